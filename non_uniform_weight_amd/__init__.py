@@ -428,3 +428,8 @@ def algorithmic_bytes(rows: int, cols: int, bits: int, nnz: int, batch: int) -> 
     if nnz > 0:
         b += 4 * nnz + 4 * (rows + 1)
     return b
+
+
+# Calls with ABI headers of their own (they use the names above).
+from .fp8 import fp8_cols, fp8_gemm, fp8_quantize, fp8_scale_pitch, fp8_workspace_bytes  # noqa: E402
+from .moe import moe_experts, moe_layer, moe_route, moe_workspace_bytes  # noqa: E402

@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "sqllm_internal.h"
 #include "sqllm_moe.h"
 
@@ -119,8 +121,27 @@ __global__ void __launch_bounds__(64) route_select(const double *__restrict__ lo
 }
 
 // ---------------------------------------------------------------------------
-// Experts.
+// Experts.  A workgroup owns 64 rows (a tile of the packed layout, lane = row)
+// of one expert in use and all the tokens that chose it; its waves share the
+// columns in half groups of 128 and add up their fp32 sums in LDS.
+//
+// Decoding without tables in memory: a row's centroids stay in registers as
+// bytes, the low bytes of the fp16 values in one set and the high bytes in
+// another, and v_perm_b32 picks four of them at once by four codes.  The
+// products of a model's experts are short (a tile of 768 to 4096 columns), so
+// the lookup tables in LDS that the long products of sqllm_device.h build per
+// tile would cost as much as they save here.
+//
+// Products: v_mfma_f32_4x4x4f16 with CBSZ = 4 multiplies each lane's own four
+// weights (B: lane = row) by the four activations of four tokens that block
+// ABID of lanes holds (A): register i of lane r ends with row r's sum for
+// token i of the quad.
 // ---------------------------------------------------------------------------
+
+typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 struct Projection {
     const uint8_t *packed;
@@ -131,67 +152,380 @@ struct Projection {
     int64_t nnz;
 };
 
-template <int BITS>
-__device__ __forceinline__ int code_of(const uint8_t *s, int c) // code c (0..255) of a group whose piece q is at s + 1024 q
-{
-    auto byte = [&](int i) { return (int)s[(i >> 4) * 1024 + (i & 15)]; };
-    const int p = c >> 1, hi = c & 1;
-    if constexpr (BITS == 4) return (byte(p) >> (4 * hi)) & 15;
-    if constexpr (BITS == 2) return (byte(p >> 1) >> (4 * (p & 1) + 2 * hi)) & 3;
-    const int u = p >> 4, q = p & 15;
-    int v;
-    if (q < 12)
-        v = byte(12 * u + q) & 63;
-    else
-        v = (byte(12 * u + q - 12) >> 6) | (byte(12 * u + 4 + q - 12) >> 6) << 2 | (byte(12 * u + 8 + q - 12) >> 6) << 4;
-    return (v >> (3 * hi)) & 7;
-}
+// v_perm_b32: result byte k is byte sel[k] of lo (0..3) or hi (4..7); 12 gives
+// 0x00, 13 gives 0xFF.
+__device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
 
-// Row `row` of expert e's matrix times v (fp16 or fp32), fp32.
-template <int BITS, typename V>
-__device__ __forceinline__ float row_product(const Projection &p, int e, int row, int rows, int cols, const V *v)
-{
-    const int lane = row & 63, groups = cols >> 8;
-    const int64_t at = (int64_t)e * rows + row;
-    const uint16_t *lut = p.lut + (at << BITS);
-    const uint8_t *base = p.packed + ((int64_t)e * (rows >> 6) + (row >> 6)) * groups * (2 * BITS * 1024) + lane * 16;
-    float acc = 0.f;
-    for (int g = 0; g < groups; ++g)
-        for (int c = 0; c < 256; ++c) {
-            const int k = code_of<BITS>(base + (int64_t)g * (2 * BITS * 1024), c);
-            acc += (float)__builtin_bit_cast(_Float16, lut[k]) * (float)v[g * 256 + c];
+// A row's centroids, split into low and high bytes, four to a register.
+template <int BITS>
+struct Table {
+    static constexpr int N = BITS == 2 ? 1 : (1 << BITS) / 4;
+    uint32_t lo[N], hi[N];
+
+    __device__ __forceinline__ void load(const uint16_t *row)
+    {
+        uint32_t w[2 * N];
+        if constexpr (BITS == 2) {
+            const u32x2 v = *(const u32x2 *)row;
+            w[0] = v.x, w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int q = 0; q < N / 2; ++q) {
+                const u32x4 v = ((const u32x4 *)row)[q];
+                w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+            }
         }
-    if (p.nnz)
-        for (int i = p.row_ptr[at]; i < p.row_ptr[at + 1]; ++i)
-            acc += (float)__builtin_bit_cast(_Float16, p.val[i]) * (float)v[p.col[i]];
-    return acc;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            lo[k] = perm(w[2 * k + 1], w[2 * k], 0x06040200);
+            hi[k] = perm(w[2 * k + 1], w[2 * k], 0x07050301);
+        }
+    }
+
+    // The centroids of four codes, one a byte of `sel` (top: the 4-bit codes'
+    // bit 3, as bytes 12 or 13 for perm; unused otherwise).
+    __device__ __forceinline__ half4_t pick(uint32_t sel, uint32_t top) const
+    {
+        uint32_t l, h;
+        if constexpr (BITS == 2) {
+            l = perm(lo[0], lo[0], sel);
+            h = perm(hi[0], hi[0], sel);
+        } else if constexpr (BITS == 3) {
+            l = perm(lo[1], lo[0], sel);
+            h = perm(hi[1], hi[0], sel);
+        } else {
+            const uint32_t mask = perm(0, 0, top);
+            const uint32_t l0 = perm(lo[1], lo[0], sel), l1 = perm(lo[3], lo[2], sel);
+            const uint32_t h0 = perm(hi[1], hi[0], sel), h1 = perm(hi[3], hi[2], sel);
+            l = (l1 & mask) | (l0 & ~mask);
+            h = (h1 & mask) | (h0 & ~mask);
+        }
+        return __builtin_bit_cast(half4_t, u32x2{perm(h, l, 0x05010400), perm(h, l, 0x07030602)});
+    }
+};
+
+// The codes of one half group (128 columns) of a lane's row, and the order in
+// which its matrix steps take the columns.  A step takes four columns; steps
+// 2n and 2n + 1 take the eight columns that lane block n holds of the
+// activations:
+//   3 and 4 bits: dword n holds columns 8n..8n+7 as four bytes of two codes;
+//     step 2n takes the first codes (columns 0, 2, 4, 6), 2n + 1 the others.
+//   2 bits: dword m holds columns 16m..16m+15 as four bytes of four codes;
+//     step 4m + i takes columns i, 4 + i, 8 + i, 12 + i.
+template <int BITS>
+struct Half {
+    uint32_t d[4 * BITS];
+
+    __device__ __forceinline__ void load(const uint8_t *src) // src: this lane's bytes of the half group's first piece
+    {
+#pragma unroll
+        for (int q = 0; q < BITS; ++q) {
+            const u32x4 v = __builtin_nontemporal_load((const u32x4 *)(src + q * 1024));
+            d[4 * q] = v.x, d[4 * q + 1] = v.y, d[4 * q + 2] = v.z, d[4 * q + 3] = v.w;
+        }
+    }
+
+    // Four bytes of two codes: pairs 4n..4n+3 of the half group (3, 4 bits).
+    template <int N>
+    __device__ __forceinline__ uint32_t pairs() const
+    {
+        if constexpr (BITS == 4) return d[N];
+        constexpr int u = 3 * (N / 4), q = N % 4;
+        if constexpr (q < 3) return d[u + q];
+        // the unit's last four pairs lie in the top two bits of its 12 bytes
+        return ((d[u] >> 6) & 0x03030303) | ((d[u + 1] >> 4) & 0x0C0C0C0C) | ((d[u + 2] >> 2) & 0x30303030);
+    }
+
+    template <int STEP>
+    __device__ __forceinline__ half4_t weights(const Table<BITS> &t) const
+    {
+        if constexpr (BITS == 2) {
+            return t.pick((d[STEP / 4] >> (2 * (STEP % 4))) & 0x03030303, 0);
+        } else {
+            const uint32_t v = pairs<STEP / 2>() >> (BITS * (STEP % 2));
+            return t.pick(v & 0x07070707, BITS == 4 ? ((v >> 3) & 0x01010101) | 0x0C0C0C0C : 0);
+        }
+    }
+};
+
+// A half group's activations of a quad of tokens: lane 4n + i holds token i's
+// values of steps 2n (x, y) and 2n + 1 (z, w) in the order above.
+template <int BITS>
+__device__ __forceinline__ u32x4 step_order(const uint16_t *x, int block) // x: the token's 128 columns
+{
+    if constexpr (BITS == 2) {
+        const u32x4 *p = (const u32x4 *)(x + 16 * (block >> 1));
+        const u32x4 a = p[0], b = p[1];
+        const bool odd = block & 1; // columns 2, 3 of each four instead of 0, 1
+        const uint32_t a0 = odd ? a.y : a.x, a1 = odd ? a.w : a.z, b0 = odd ? b.y : b.x, b1 = odd ? b.w : b.z;
+        return u32x4{perm(a1, a0, 0x05040100), perm(b1, b0, 0x05040100), perm(a1, a0, 0x07060302),
+                     perm(b1, b0, 0x07060302)};
+    } else {
+        const u32x4 v = *(const u32x4 *)(x + 8 * block);
+        return u32x4{perm(v.y, v.x, 0x05040100), perm(v.w, v.z, 0x05040100), perm(v.y, v.x, 0x07060302),
+                     perm(v.w, v.z, 0x07060302)};
+    }
 }
 
-// a[pair][inter]: gate and up of one 64-row tile for one (token, choice).
-template <int BITS>
-__global__ void __launch_bounds__(64) experts_gate_up(Projection gate, Projection up, const uint16_t *x,
-                                                      const int32_t *ids, int experts, int topk, int hidden, int inter,
-                                                      float *a)
+// The experts in use, each once and in ascending order, are the launch's grid
+// rows: which expert row `slot` is, and which tokens chose it.  Every wave
+// works it out for itself from ids[] (at most 128), without a barrier: a
+// bitmap of the experts, its running count, and two ballots.
+// Orders a wave's own LDS accesses (its LDS instructions run in order; the
+// compiler may not move them across this).
+__device__ __forceinline__ void wave_sync()
 {
-    const int pair = blockIdx.y, row = blockIdx.x * 64 + threadIdx.x, e = ids[pair];
-    if (e < 0 || e >= experts) return;
-    const _Float16 *v = (const _Float16 *)x + (int64_t)(pair / topk) * hidden;
-    const float g = row_product<BITS>(gate, e, row, inter, hidden, v);
-    const float u = row_product<BITS>(up, e, row, inter, hidden, v);
-    a[(int64_t)pair * inter + row] = g / (1.f + __expf(-g)) * u;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(64) experts_down(Projection down, const float *a, const int32_t *ids,
-                                                   const float *weights, int experts, int topk, int hidden, int inter,
-                                                   uint16_t *y)
+struct Chosen {
+    int expert; // -1: fewer experts are in use
+    int count;  // tokens that chose it
+};
+
+struct ChosenLds {
+    uint32_t bitmap[kMaxExperts / 32];
+    uint32_t list[kMaxBatch]; // token | first of its choices << 8
+};
+
+__device__ __forceinline__ Chosen find_chosen(const int32_t *ids, int pairs, int topk, int batch, int experts, int slot,
+                                              ChosenLds &lds)
 {
-    const int t = blockIdx.y, row = blockIdx.x * 64 + threadIdx.x;
+    const int lane = threadIdx.x & 63;
+    auto id_of = [&](int p) {
+        const int e = p < pairs ? ids[p] : -1;
+        return e < experts ? e : -1;
+    };
+    const int e0 = id_of(lane), e1 = id_of(lane + 64);
+    if (lane < kMaxExperts / 32) lds.bitmap[lane] = 0;
+    wave_sync();
+    if (e0 >= 0) atomicOr(&lds.bitmap[e0 >> 5], 1u << (e0 & 31));
+    if (e1 >= 0) atomicOr(&lds.bitmap[e1 >> 5], 1u << (e1 & 31));
+    wave_sync();
+    const uint32_t word = lane < kMaxExperts / 32 ? lds.bitmap[lane] : 0;
+    int before = __popc(word); // running count over the sixteen words
+#pragma unroll
+    for (int m = 1; m < kMaxExperts / 32; m <<= 1) {
+        const int o = __shfl_up(before, m);
+        if (lane >= m) before += o;
+    }
+    const uint64_t past = __ballot(lane < kMaxExperts / 32 && before > slot);
+    if (past == 0) return {-1, 0};
+    const int at = __builtin_ctzll(past);
+    uint32_t w = __builtin_amdgcn_readlane(word, at);
+    for (int skip = slot - (__builtin_amdgcn_readlane(before, at) - __popc(w)); skip > 0; --skip) w &= w - 1;
+    const int e = 32 * at + __builtin_ctz(w);
+    const uint64_t m0 = __ballot(e0 == e), m1 = __ballot(e1 == e);
+    // lane t: token t's choices are bits t * topk .. of the 128
+    const int sh = lane * topk;
+    uint64_t bits = 0;
+    if (lane < batch) bits = sh >= 64 ? m1 >> (sh - 64) : (m0 >> sh) | (sh ? m1 << (64 - sh) : 0);
+    bits &= (1ull << topk) - 1;
+    const uint64_t tokens = __ballot(bits != 0);
+    if (bits) lds.list[__popcll(tokens & ((1ull << lane) - 1))] = lane | (__builtin_ctzll(bits) << 8);
+    wave_sync();
+    return {e, (int)__popcll(tokens)};
+}
+
+// This wave's share of one matrix for one tile: half groups first, first +
+// step, ... below `end`, and nonzeros share, share + shares, ... of each row.
+// x(j) is the fp16 row of batch column j.  acc[h][i]: column 4h + i.
+template <int BITS, int NQ>
+struct Accumulators {
+    f32x4 even[NQ], odd[NQ]; // two chains, so that a matrix step does not wait for the one before it
+};
+
+template <int BITS, int NQ, typename X>
+__device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int64_t row, int groups, int first,
+                                             int end, int step, int share, int shares, int columns, X x,
+                                             float (&sum)[4 * NQ])
+{
+    constexpr int D = NQ <= 2 ? 3 : (NQ <= 4 ? 2 : 1); // half groups in flight
+    const int lane = threadIdx.x & 63, block = lane >> 2;
+    Table<BITS> table;
+    table.load(p.lut + (row << BITS));
+    int lo = 0, hi = 0;
+    if (p.nnz) lo = p.row_ptr[row] + share, hi = p.row_ptr[row + 1];
+    const uint8_t *codes = p.packed + tile * groups * (2 * BITS * 1024) + lane * 16;
+    const uint16_t *xr[NQ];
+#pragma unroll
+    for (int h = 0; h < NQ; ++h) xr[h] = x(min(4 * h + (lane & 3), columns - 1)); // past the last: a copy, dropped
+    Half<BITS> ring[D];
+    u32x4 xq[D][NQ];
+    auto load = [&](int k, int g) {
+        ring[k].load(codes + (int64_t)g * (BITS * 1024));
+#pragma unroll
+        for (int h = 0; h < NQ; ++h) xq[k][h] = step_order<BITS>(xr[h] + 128 * g, block);
+    };
+    Accumulators<BITS, NQ> acc;
+#pragma unroll
+    for (int h = 0; h < NQ; ++h) acc.even[h] = acc.odd[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](int k) {
+        [&]<int... Ns>(std::integer_sequence<int, Ns...>) {
+            (
+                [&] {
+                    const half4_t we = ring[k].template weights<2 * Ns>(table);
+                    const half4_t wo = ring[k].template weights<2 * Ns + 1>(table);
+#pragma unroll
+                    for (int h = 0; h < NQ; ++h) {
+                        const half4_t xe = __builtin_bit_cast(half4_t, u32x2{xq[k][h].x, xq[k][h].y});
+                        const half4_t xo = __builtin_bit_cast(half4_t, u32x2{xq[k][h].z, xq[k][h].w});
+                        acc.even[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(xe, we, acc.even[h], 4, Ns, 0);
+                        acc.odd[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(xo, wo, acc.odd[h], 4, Ns, 0);
+                    }
+                }(),
+                ...);
+        }(std::make_integer_sequence<int, 16>{});
+    };
+#pragma unroll
+    for (int k = 0; k < D; ++k)
+        if (first + k * step < end) load(k, first + k * step);
+    for (int g = first; g < end; g += D * step) {
+#pragma unroll
+        for (int k = 0; k < D; ++k) {
+            if (g + k * step < end) multiply(k);
+            if (g + (k + D) * step < end) load(k, g + (k + D) * step);
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < NQ; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[4 * h + i] = acc.even[h][i] + acc.odd[h][i];
+    // outliers: lane = row walks its share of the row's nonzeros (the waves
+    // share every row, so a row with many is spread too)
+    for (int i = lo; i < hi; i += shares) {
+        const float v = (float)__builtin_bit_cast(_Float16, p.val[i]);
+        const int c = p.col[i];
+#pragma unroll
+        for (int j = 0; j < 4 * NQ; ++j)
+            if (j < columns) sum[j] += v * (float)__builtin_bit_cast(_Float16, x(j)[c]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// a = silu(gate x) * (up x), split into two fp16 values per entry: the lower
+// 11 bits cost the second product another matrix step, and storing a in one
+// fp16 value would cost it half of its accuracy.
+// Grid (inter / 64, experts in use at most); even waves take gate, odd ones up.
+// ---------------------------------------------------------------------------
+template <int BITS, int NQ>
+__device__ __forceinline__ void gate_up_body(const Projection &gate, const Projection &up, const uint16_t *x,
+                                             const ChosenLds &lds, Chosen c, int topk, int hidden, int inter,
+                                             int64_t pairs, uint16_t *a, float *red)
+{
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    const int64_t tile = (int64_t)c.expert * (inter >> 6) + blockIdx.x, row = tile * 64 + lane;
+    float sum[4 * NQ];
+    tile_product<BITS, NQ>(w & 1 ? up : gate, tile, row, hidden >> 8, w >> 1, hidden >> 7, waves >> 1, w >> 1, waves >> 1,
+                           c.count, [&](int j) { return x + (int64_t)(lds.list[j] & 255) * hidden; }, sum);
+#pragma unroll
+    for (int j = 0; j < 4 * NQ; ++j) red[(w * 4 * NQ + j) * 64 + lane] = sum[j];
+    __syncthreads();
+    for (int j = w; j < c.count; j += waves) {
+        float g = 0.f, u = 0.f;
+        for (int k = 0; k < waves; k += 2) {
+            g += red[(k * 4 * NQ + j) * 64 + lane];
+            u += red[((k + 1) * 4 * NQ + j) * 64 + lane];
+        }
+        const float v = g / (1.f + expf(-g)) * u;
+        const _Float16 hi = (_Float16)v;
+        const float rest = fabsf(v) < 65520.f ? v - (float)hi : 0.f; // beyond, hi is infinite or NaN already
+        const int64_t pair = (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8);
+        a[pair * inter + blockIdx.x * 64 + lane] = __builtin_bit_cast(uint16_t, hi);
+        a[(pairs + pair) * inter + blockIdx.x * 64 + lane] = __builtin_bit_cast(uint16_t, (_Float16)rest);
+    }
+}
+
+template <int BITS, int MAXQ>
+__global__ void __launch_bounds__(kMaxWaves * 64) experts_gate_up(Projection gate, Projection up, const uint16_t *x,
+                                                                  const int32_t *ids, int batch, int experts, int topk,
+                                                                  int hidden, int inter, uint16_t *a)
+{
+    __shared__ ChosenLds chosen[kMaxWaves];
+    extern __shared__ float red[];
+    ChosenLds &lds = chosen[threadIdx.x >> 6];
+    const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
+    if (c.expert < 0) return;
+    const int64_t pairs = batch * topk;
+    if (MAXQ >= 4 && c.count > 8)
+        gate_up_body<BITS, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, pairs, a, red);
+    else if (MAXQ >= 2 && c.count > 4)
+        gate_up_body<BITS, MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, pairs, a, red);
+    else
+        gate_up_body<BITS, 1>(gate, up, x, lds, c, topk, hidden, inter, pairs, a, red);
+}
+
+// ---------------------------------------------------------------------------
+// part[split][pair][hidden] = down a, fp32, over the split's columns.  A
+// token's two fp16 values stand in quads h and NQ / 2 + h.
+// Grid (hidden / 64 * splits, experts in use at most).
+// ---------------------------------------------------------------------------
+template <int BITS, int NQ>
+__device__ __forceinline__ void down_body(const Projection &down, const uint16_t *a, const ChosenLds &lds, Chosen c,
+                                          int topk, int hidden, int inter, int splits, int64_t pairs, float *part,
+                                          float *red)
+{
+    constexpr int T = 2 * NQ; // tokens
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, waves = blockDim.x >> 6;
+    const int tiles = hidden >> 6, split = blockIdx.x / tiles, t = blockIdx.x - split * tiles;
+    const int64_t tile = (int64_t)c.expert * tiles + t, row = tile * 64 + lane;
+    auto pair_of = [&](int j) { return (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8); };
+    float sum[4 * NQ];
+    const int workers = waves * splits, worker = split * waves + w;
+    tile_product<BITS, NQ>(down, tile, row, inter >> 8, worker, inter >> 7, workers, worker, workers, 4 * NQ,
+                           [&](int j) { return a + ((j >= T ? pairs : 0) + pair_of(min(j % T, c.count - 1))) * inter; }, sum);
+#pragma unroll
+    for (int j = 0; j < T; ++j) red[(w * T + j) * 64 + lane] = sum[j] + sum[T + j];
+    __syncthreads();
+    for (int j = w; j < c.count; j += waves) {
+        float v = 0.f;
+        for (int k = 0; k < waves; ++k) v += red[(k * T + j) * 64 + lane];
+        part[((int64_t)split * pairs + pair_of(j)) * hidden + t * 64 + lane] = v;
+    }
+}
+
+template <int BITS, int MAXQ>
+__global__ void __launch_bounds__(kMaxWaves * 64) experts_down(Projection down, const uint16_t *a, const int32_t *ids,
+                                                               int batch, int experts, int topk, int hidden, int inter,
+                                                               int splits, float *part)
+{
+    __shared__ ChosenLds chosen[kMaxWaves];
+    extern __shared__ float red[];
+    ChosenLds &lds = chosen[threadIdx.x >> 6];
+    const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
+    if (c.expert < 0) return;
+    const int64_t pairs = batch * topk;
+    if (MAXQ >= 4 && c.count > 8)
+        down_body<BITS, MAXQ >= 4 ? 8 : 2>(down, a, lds, c, topk, hidden, inter, splits, pairs, part, red);
+    else if (MAXQ >= 2 && c.count > 4)
+        down_body<BITS, MAXQ >= 2 ? 4 : 2>(down, a, lds, c, topk, hidden, inter, splits, pairs, part, red);
+    else
+        down_body<BITS, 2>(down, a, lds, c, topk, hidden, inter, splits, pairs, part, red);
+}
+
+// y = the weighted sum of a token's partial sums, in the order of its choices;
+// a repeated id's partial sums stand at its first choice.
+__global__ void __launch_bounds__(256) experts_combine(const float *part, const int32_t *ids, const float *weights,
+                                                       int batch, int experts, int topk, int hidden, int splits,
+                                                       uint16_t *y)
+{
+    const int t = blockIdx.y, row = blockIdx.x * 256 + threadIdx.x;
     float sum = 0.f;
     for (int k = 0; k < topk; ++k) {
-        const int pair = t * topk + k, e = ids[pair];
+        const int e = ids[t * topk + k];
         if (e < 0 || e >= experts) continue;
-        sum += weights[pair] * row_product<BITS>(down, e, row, hidden, inter, a + (int64_t)pair * inter);
+        float w = 0.f;
+        bool first = true;
+        for (int o = 0; o < topk; ++o)
+            if (ids[t * topk + o] == e) {
+                if (o < k) first = false;
+                w += weights[t * topk + o];
+            }
+        if (!first) continue;
+        float v = 0.f;
+        for (int s = 0; s < splits; ++s) v += part[((int64_t)s * batch * topk + t * topk + k) * hidden + row];
+        sum += w * v;
     }
     y[(int64_t)t * hidden + row] = __builtin_bit_cast(uint16_t, (_Float16)sum);
 }
@@ -212,15 +546,29 @@ sqllm_status check_sizes(int batch, int experts, int topk, int64_t hidden, int64
     return SQLLM_OK;
 }
 
+int64_t used_at_most(int batch, int experts, int topk) { return batch * topk < experts ? batch * topk : experts; }
+
+// Workgroups that share a down tile's columns: more than one only while the
+// launch would leave compute units without work and every wave keeps at
+// least two half groups.
+int down_splits(int batch, int experts, int topk, int64_t hidden, int64_t inter)
+{
+    int s = 1;
+    while (s < 8 && used_at_most(batch, experts, topk) * (hidden / 64) * s < 256 && inter / 128 >= 4 * kDefaultWaves * s) s *= 2;
+    return s;
+}
+
 // Scratch of one call, in this order.
 struct Layout {
-    size_t logits, act, end;
-    Layout(int batch, int experts, int topk, int64_t inter)
+    size_t logits, act, part, end;
+    Layout(int batch, int experts, int topk, int64_t hidden, int64_t inter)
     {
         auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+        const size_t pairs = (size_t)batch * topk;
         logits = 0;
         act = up((size_t)batch * experts * 8);
-        end = act + up((size_t)batch * topk * inter * 4);
+        part = act + up(pairs * inter * 4);
+        end = part + up(pairs * hidden * 4 * down_splits(batch, experts, topk, hidden, inter));
     }
 };
 
@@ -280,16 +628,22 @@ Projection projection(const sqllm_experts &p)
     return {(const uint8_t *)p.packed, p.lut, p.row_ptr, p.col_idx, p.val, p.nnz};
 }
 
-template <int BITS>
+template <int BITS, int MAXQ>
 sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weights, const Projection &gate,
                       const Projection &up, const Projection &down, int batch, int experts, int topk, int hidden,
                       int inter, uint16_t *y, const Layout &at, char *ws, hipStream_t stream)
 {
-    float *a = (float *)(ws + at.act);
-    hipLaunchKernelGGL((experts_gate_up<BITS>), dim3(inter / 64, batch * topk), dim3(64), 0, stream, gate, up, x, ids,
-                       experts, topk, hidden, inter, a);
-    hipLaunchKernelGGL((experts_down<BITS>), dim3(hidden / 64, batch), dim3(64), 0, stream, down, a, ids, weights,
-                       experts, topk, hidden, inter, y);
+    uint16_t *a = (uint16_t *)(ws + at.act);
+    float *part = (float *)(ws + at.part);
+    const int used = (int)used_at_most(batch, experts, topk), splits = down_splits(batch, experts, topk, hidden, inter);
+    const int waves = kDefaultWaves;
+    const size_t red = (size_t)waves * 4 * MAXQ * 64 * sizeof(float);
+    hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(inter / 64, used), dim3(64 * waves), red, stream, gate, up, x,
+                       ids, batch, experts, topk, hidden, inter, a);
+    hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(hidden / 64 * splits, used), dim3(64 * waves), red, stream, down,
+                       a, ids, batch, experts, topk, hidden, inter, splits, part);
+    hipLaunchKernelGGL(experts_combine, dim3(hidden / 256, batch), dim3(256), 0, stream, part, ids, weights, batch,
+                       experts, topk, hidden, splits, y);
     return launched();
 }
 
@@ -298,7 +652,11 @@ sqllm_status products_of(int bits, const uint16_t *x, const int32_t *ids, const 
                          int experts, int topk, int64_t hidden, int64_t inter, uint16_t *y, const Layout &at, char *ws,
                          hipStream_t stream)
 {
-    auto run = bits == 2 ? products<2> : bits == 3 ? products<3> : products<4>;
+    const int q = batch > 8 ? 2 : batch > 4 ? 1 : 0;
+    decltype(&products<2, 1>) of[3][3] = {{products<2, 1>, products<2, 2>, products<2, 4>},
+                                          {products<3, 1>, products<3, 2>, products<3, 4>},
+                                          {products<4, 1>, products<4, 2>, products<4, 4>}};
+    auto run = of[bits - 2][q];
     return run(x, ids, weights, projection(*gate), projection(*up), projection(*down), batch, experts, topk,
                (int)hidden, (int)inter, y, at, ws, stream);
 }
@@ -308,7 +666,7 @@ sqllm_status products_of(int bits, const uint16_t *x, const int32_t *ids, const 
 extern "C" size_t sqllm_moe_workspace_bytes(int batch, int experts, int topk, int64_t hidden, int64_t inter)
 {
     if (check_sizes(batch, experts, topk, hidden, inter) != SQLLM_OK) return 0;
-    return Layout(batch, experts, topk, inter).end;
+    return Layout(batch, experts, topk, hidden, inter).end;
 }
 
 extern "C" sqllm_status sqllm_moe_route(const uint16_t *x, const uint16_t *router, const float *bias, int batch,
@@ -318,7 +676,7 @@ extern "C" sqllm_status sqllm_moe_route(const uint16_t *x, const uint16_t *route
     sqllm_status st = check_route(x, router, bias, flags, ids, weights);
     if (st == SQLLM_OK) st = check_sizes(batch, experts, topk, hidden, kGroupCols);
     if (st != SQLLM_OK) return st;
-    const Layout at(batch, experts, topk, kGroupCols);
+    const Layout at(batch, experts, topk, hidden, kGroupCols);
     st = check_workspace(workspace, workspace_bytes, at.end);
     if (st != SQLLM_OK) return st;
     return route(x, router, bias, batch, experts, hidden, topk, flags, scale, ids, weights, at, (char *)workspace,
@@ -334,7 +692,7 @@ extern "C" sqllm_status sqllm_moe_experts(const uint16_t *x, const int32_t *ids,
     sqllm_status st = check_products(x, ids, weights, gate, up, down, bits, y);
     if (st == SQLLM_OK) st = check_sizes(batch, experts, topk, hidden, inter);
     if (st != SQLLM_OK) return st;
-    const Layout at(batch, experts, topk, inter);
+    const Layout at(batch, experts, topk, hidden, inter);
     st = check_workspace(workspace, workspace_bytes, at.end);
     if (st != SQLLM_OK) return st;
     return products_of(bits, x, ids, weights, gate, up, down, batch, experts, topk, hidden, inter, y, at,
@@ -351,7 +709,7 @@ extern "C" sqllm_status sqllm_moe_layer(const uint16_t *x, const uint16_t *route
     if (st == SQLLM_OK) st = check_products(x, ids, weights, gate, up, down, bits, y);
     if (st == SQLLM_OK) st = check_sizes(batch, experts, topk, hidden, inter);
     if (st != SQLLM_OK) return st;
-    const Layout at(batch, experts, topk, inter);
+    const Layout at(batch, experts, topk, hidden, inter);
     st = check_workspace(workspace, workspace_bytes, at.end);
     if (st != SQLLM_OK) return st;
     st = route(x, router, bias, batch, experts, hidden, topk, flags, scale, ids, weights, at, (char *)workspace, stream);

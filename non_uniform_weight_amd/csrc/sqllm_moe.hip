@@ -10,6 +10,7 @@
 
 #include <utility>
 
+#include "sqllm_device.h"
 #include "sqllm_internal.h"
 #include "sqllm_moe.h"
 
@@ -138,10 +139,10 @@ __global__ void __launch_bounds__(64) route_select(const double *__restrict__ lo
 // token i of the quad.
 // ---------------------------------------------------------------------------
 
-typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+using dev::f32x4;
+using dev::half4_t;
+using dev::u32x2;
+using dev::u32x4;
 
 struct Projection {
     const uint8_t *packed;
@@ -152,8 +153,8 @@ struct Projection {
     int64_t nnz;
 };
 
-// v_perm_b32: result byte k is byte sel[k] of lo (0..3) or hi (4..7); 12 gives
-// 0x00, 13 gives 0xFF.
+// v_perm_b32: result byte k is byte sel[k] of lo (0..3) or hi (4..7); 8, 9, 10
+// and 11 repeat the top bit of bytes 1 and 3 of lo and of hi.
 __device__ __forceinline__ uint32_t perm(uint32_t hi, uint32_t lo, uint32_t sel) { return __builtin_amdgcn_perm(hi, lo, sel); }
 
 // A row's centroids, split into low and high bytes, four to a register.
@@ -182,9 +183,9 @@ struct Table {
         }
     }
 
-    // The centroids of four codes, one a byte of `sel` (top: the 4-bit codes'
-    // bit 3, as bytes 12 or 13 for perm; unused otherwise).
-    __device__ __forceinline__ half4_t pick(uint32_t sel, uint32_t top) const
+    // The centroids of four codes, one a byte of `sel` (the low three bits);
+    // at 4 bits `upper` has 0xFF in the bytes of the codes from 8 on.
+    __device__ __forceinline__ half4_t pick(uint32_t sel, uint32_t upper) const
     {
         uint32_t l, h;
         if constexpr (BITS == 2) {
@@ -194,11 +195,10 @@ struct Table {
             l = perm(lo[1], lo[0], sel);
             h = perm(hi[1], hi[0], sel);
         } else {
-            const uint32_t mask = perm(0, 0, top);
             const uint32_t l0 = perm(lo[1], lo[0], sel), l1 = perm(lo[3], lo[2], sel);
             const uint32_t h0 = perm(hi[1], hi[0], sel), h1 = perm(hi[3], hi[2], sel);
-            l = (l1 & mask) | (l0 & ~mask);
-            h = (h1 & mask) | (h0 & ~mask);
+            l = (l1 & upper) | (l0 & ~upper);
+            h = (h1 & upper) | (h0 & ~upper);
         }
         return __builtin_bit_cast(half4_t, u32x2{perm(h, l, 0x05010400), perm(h, l, 0x07030602)});
     }
@@ -242,8 +242,12 @@ struct Half {
         if constexpr (BITS == 2) {
             return t.pick((d[STEP / 4] >> (2 * (STEP % 4))) & 0x03030303, 0);
         } else {
-            const uint32_t v = pairs<STEP / 2>() >> (BITS * (STEP % 2));
-            return t.pick(v & 0x07070707, BITS == 4 ? ((v >> 3) & 0x01010101) | 0x0C0C0C0C : 0);
+            const uint32_t v = pairs<STEP / 2>();
+            // the codes' bit 3 to every bit of their bytes: perm's selectors 8
+            // to 11 repeat the top bit of the operands' bytes 1 and 3
+            uint32_t upper = 0;
+            if constexpr (BITS == 4) upper = STEP % 2 ? perm(v, v << 8, 0x0B090A08) : perm(v << 4, v << 12, 0x0B090A08);
+            return t.pick((v >> (BITS * (STEP % 2))) & 0x07070707, upper);
         }
     }
 };
@@ -328,29 +332,51 @@ __device__ __forceinline__ Chosen find_chosen(const int32_t *ids, int pairs, int
     return {e, (int)__popcll(tokens)};
 }
 
-// This wave's share of one matrix for one tile: half groups first, first +
-// step, ... below `end`, and nonzeros share, share + shares, ... of each row.
-// x(j) is the fp16 row of batch column j.  acc[h][i]: column 4h + i.
+// Adds one chunk of 64 nonzeros [cb, min(cb + 64, v1)) of a tile (lane's value
+// val and activation x; rows non-decreasing over the lanes) to the row lanes'
+// sums: an inclusive prefix sum over the wave, of which a row takes the
+// difference over its run of lanes [rp_lo, rp_hi).
+__device__ __forceinline__ void add_chunk(uint32_t val, float x, int cb, int v1, int lane, int rp_lo, int rp_hi, float &sum)
+{
+    float v = cb + lane < v1 ? dev::f16_to_f32((uint16_t)val) * x : 0.f;
+    v += dev::row_shr<1>(v);
+    v += dev::row_shr<2>(v);
+    v += dev::row_shr<4>(v);
+    v += dev::row_shr<8>(v);
+    v += dev::row_bcast15(v);
+    v += dev::row_bcast31(v);
+    const int first = max(rp_lo, cb) - cb, last = min(min(rp_hi, cb + 64), v1) - 1 - cb;
+    const bool present = first <= last;
+    const float top = dev::lane_read(present ? last : 0, v), below = dev::lane_read(present && first > 0 ? first - 1 : 0, v);
+    if (present) sum += first > 0 ? top - below : top;
+}
+
+// This wave's share (worker `worker` of `workers`) of one matrix for one tile:
+// every workers-th half group, and a contiguous range of the tile's nonzeros.
+// x(j) is the fp16 row of matrix column j, and value(j, c) the activation of
+// token j at column c in fp32, for the outliers of tokens below `tokens`.
+// Column 4h + i of the matrix steps ends in sum[4h + i]; an outlier of token j
+// is added to sum[j].
 template <int BITS, int NQ>
 struct Accumulators {
     f32x4 even[NQ], odd[NQ]; // two chains, so that a matrix step does not wait for the one before it
 };
 
-template <int BITS, int NQ, typename X>
-__device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int64_t row, int groups, int first,
-                                             int end, int step, int share, int shares, int columns, X x,
-                                             float (&sum)[4 * NQ])
+template <int BITS, int NQ, int T, typename X, typename V>
+__device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int groups, int worker, int workers,
+                                             int tokens, X x, V value, float (&sum)[4 * NQ])
 {
     constexpr int D = NQ <= 2 ? 3 : (NQ <= 4 ? 2 : 1); // half groups in flight
-    const int lane = threadIdx.x & 63, block = lane >> 2;
+    const int lane = threadIdx.x & 63, block = lane >> 2, end = 2 * groups;
+    const int64_t row = tile * 64 + lane;
     Table<BITS> table;
     table.load(p.lut + (row << BITS));
-    int lo = 0, hi = 0;
-    if (p.nnz) lo = p.row_ptr[row] + share, hi = p.row_ptr[row + 1];
+    int rp_lo = 0, rp_hi = 0;
+    if (p.nnz) rp_lo = p.row_ptr[row], rp_hi = p.row_ptr[row + 1];
     const uint8_t *codes = p.packed + tile * groups * (2 * BITS * 1024) + lane * 16;
     const uint16_t *xr[NQ];
 #pragma unroll
-    for (int h = 0; h < NQ; ++h) xr[h] = x(min(4 * h + (lane & 3), columns - 1)); // past the last: a copy, dropped
+    for (int h = 0; h < NQ; ++h) xr[h] = x(4 * h + (lane & 3));
     Half<BITS> ring[D];
     u32x4 xq[D][NQ];
     auto load = [&](int k, int g) {
@@ -380,51 +406,84 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
     };
 #pragma unroll
     for (int k = 0; k < D; ++k)
-        if (first + k * step < end) load(k, first + k * step);
-    for (int g = first; g < end; g += D * step) {
+        if (worker + k * workers < end) load(k, worker + k * workers);
+    for (int g = worker; g < end; g += D * workers) {
 #pragma unroll
         for (int k = 0; k < D; ++k) {
-            if (g + k * step < end) multiply(k);
-            if (g + (k + D) * step < end) load(k, g + (k + D) * step);
+            if (g + k * workers < end) multiply(k);
+            if (g + (k + D) * workers < end) load(k, g + (k + D) * workers);
         }
     }
 #pragma unroll
     for (int h = 0; h < NQ; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[4 * h + i] = acc.even[h][i] + acc.odd[h][i];
-    // outliers: lane = row walks its share of the row's nonzeros (the waves
-    // share every row, so a row with many is spread too)
-    for (int i = lo; i < hi; i += shares) {
-        const float v = (float)__builtin_bit_cast(_Float16, p.val[i]);
-        const int c = p.col[i];
+    // outliers: a nonzero per lane, kChunks of 64 at a time so that a round
+    // waits for memory twice; a prefix sum over the wave gives every row's
+    // run of products as a difference
+    if (p.nnz == 0) return;
+    constexpr int kChunks = 4;
+    const int nz0 = __builtin_amdgcn_readfirstlane(rp_lo); // all else relative to the tile's first nonzero
+    rp_lo -= nz0, rp_hi -= nz0;
+    const int len = __builtin_amdgcn_readlane(rp_hi, 63), per = len / workers, extra = len - per * workers;
+    const int v0 = worker * per + min(worker, extra), v1 = v0 + per + (worker < extra ? 1 : 0);
+    const uint16_t *cols = p.col + nz0, *vals = p.val + nz0;
+    for (int base = v0; base < v1; base += 64 * kChunks) {
+        int col[kChunks];
+        uint32_t val[kChunks];
 #pragma unroll
-        for (int j = 0; j < 4 * NQ; ++j)
-            if (j < columns) sum[j] += v * (float)__builtin_bit_cast(_Float16, x(j)[c]);
+        for (int k = 0; k < kChunks; ++k) { // past the last: that one again, dropped by the scan
+            const int n = min(base + 64 * k + lane, v1 - 1);
+            col[k] = cols[n];
+            val[k] = vals[n];
+        }
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            if (j < tokens) {
+                float xv[kChunks];
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k) xv[k] = value(j, col[k]);
+#pragma unroll
+                for (int k = 0; k < kChunks; ++k)
+                    if (base + 64 * k < v1) add_chunk(val[k], xv[k], base + 64 * k, v1, lane, rp_lo, rp_hi, sum[j]);
+            }
     }
 }
 
 // ---------------------------------------------------------------------------
-// a = silu(gate x) * (up x), split into two fp16 values per entry: the lower
-// 11 bits cost the second product another matrix step, and storing a in one
-// fp16 value would cost it half of its accuracy.
-// Grid (inter / 64, experts in use at most); even waves take gate, odd ones up.
+// a = silu(gate x) * (up x), split into two fp16 values per entry for the
+// matrix steps of down (storing a in one would double the error of y) and
+// whole for its outliers.
+// `parts` waves share a tile, the even ones gate and the odd ones up; the
+// eight waves of a workgroup have neighbouring tiles of one expert.
+// Grid (inter / 64 / (8 / parts), experts in use at most).
 // ---------------------------------------------------------------------------
+struct Activations { // [pair][inter]
+    uint16_t *hi, *lo;
+    float *whole;
+};
+
 template <int BITS, int NQ>
 __device__ __forceinline__ void gate_up_body(const Projection &gate, const Projection &up, const uint16_t *x,
                                              const ChosenLds &lds, Chosen c, int topk, int hidden, int inter,
-                                             int64_t pairs, uint16_t *a, float *red)
+                                             int parts, Activations a, float *red)
 {
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-    const int64_t tile = (int64_t)c.expert * (inter >> 6) + blockIdx.x, row = tile * 64 + lane;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int part = w & (parts - 1), t = blockIdx.x * (kDefaultWaves / parts) + w / parts;
+    const int64_t tile = (int64_t)c.expert * (inter >> 6) + t;
+    auto row_of = [&](int j) { return x + (int64_t)(lds.list[j] & 255) * hidden; };
     float sum[4 * NQ];
-    tile_product<BITS, NQ>(w & 1 ? up : gate, tile, row, hidden >> 8, w >> 1, hidden >> 7, waves >> 1, w >> 1, waves >> 1,
-                           c.count, [&](int j) { return x + (int64_t)(lds.list[j] & 255) * hidden; }, sum);
+    tile_product<BITS, NQ, 4 * NQ>(
+        part & 1 ? up : gate, tile, hidden >> 8, part >> 1, parts >> 1, c.count,
+        [&](int j) { return row_of(min(j, c.count - 1)); }, // past the last: a copy, whose sums are dropped
+        [&](int j, int col) { return dev::f16_to_f32(row_of(j)[col]); }, sum);
 #pragma unroll
     for (int j = 0; j < 4 * NQ; ++j) red[(w * 4 * NQ + j) * 64 + lane] = sum[j];
     __syncthreads();
-    for (int j = w; j < c.count; j += waves) {
+    const int w0 = w - part;
+    for (int j = part; j < c.count; j += parts) {
         float g = 0.f, u = 0.f;
-        for (int k = 0; k < waves; k += 2) {
+        for (int k = w0; k < w0 + parts; k += 2) {
             g += red[(k * 4 * NQ + j) * 64 + lane];
             u += red[((k + 1) * 4 * NQ + j) * 64 + lane];
         }
@@ -432,76 +491,93 @@ __device__ __forceinline__ void gate_up_body(const Projection &gate, const Proje
         const _Float16 hi = (_Float16)v;
         const float rest = fabsf(v) < 65520.f ? v - (float)hi : 0.f; // beyond, hi is infinite or NaN already
         const int64_t pair = (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8);
-        a[pair * inter + blockIdx.x * 64 + lane] = __builtin_bit_cast(uint16_t, hi);
-        a[(pairs + pair) * inter + blockIdx.x * 64 + lane] = __builtin_bit_cast(uint16_t, (_Float16)rest);
+        const int64_t at = pair * inter + t * 64 + lane;
+        a.hi[at] = __builtin_bit_cast(uint16_t, hi);
+        a.lo[at] = __builtin_bit_cast(uint16_t, (_Float16)rest);
+        a.whole[at] = v;
     }
 }
 
 template <int BITS, int MAXQ>
-__global__ void __launch_bounds__(kMaxWaves * 64) experts_gate_up(Projection gate, Projection up, const uint16_t *x,
+__global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Projection gate, Projection up, const uint16_t *x,
                                                                   const int32_t *ids, int batch, int experts, int topk,
-                                                                  int hidden, int inter, uint16_t *a)
+                                                                  int hidden, int inter, int parts, Activations a)
 {
-    __shared__ ChosenLds chosen[kMaxWaves];
+    __shared__ ChosenLds chosen[kDefaultWaves];
     extern __shared__ float red[];
     ChosenLds &lds = chosen[threadIdx.x >> 6];
     const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
     if (c.expert < 0) return;
-    const int64_t pairs = batch * topk;
     if (MAXQ >= 4 && c.count > 8)
-        gate_up_body<BITS, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, pairs, a, red);
+        gate_up_body<BITS, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, parts, a, red);
     else if (MAXQ >= 2 && c.count > 4)
-        gate_up_body<BITS, MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, pairs, a, red);
+        gate_up_body<BITS, MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, parts, a, red);
     else
-        gate_up_body<BITS, 1>(gate, up, x, lds, c, topk, hidden, inter, pairs, a, red);
+        gate_up_body<BITS, 1>(gate, up, x, lds, c, topk, hidden, inter, parts, a, red);
 }
 
 // ---------------------------------------------------------------------------
 // part[split][pair][hidden] = down a, fp32, over the split's columns.  A
-// token's two fp16 values stand in quads h and NQ / 2 + h.
-// Grid (hidden / 64 * splits, experts in use at most).
+// token j's two fp16 values stand in columns j and 2 NQ + j.  `parts` waves
+// share a tile and split, as above.
+// Grid (ceil(hidden / 64 / (8 / parts)), experts in use at most, splits).
 // ---------------------------------------------------------------------------
 template <int BITS, int NQ>
-__device__ __forceinline__ void down_body(const Projection &down, const uint16_t *a, const ChosenLds &lds, Chosen c,
-                                          int topk, int hidden, int inter, int splits, int64_t pairs, float *part,
+__device__ __forceinline__ void down_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
+                                          int topk, int hidden, int inter, int parts, int64_t pairs, float *partial,
                                           float *red)
 {
     constexpr int T = 2 * NQ; // tokens
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, waves = blockDim.x >> 6;
-    const int tiles = hidden >> 6, split = blockIdx.x / tiles, t = blockIdx.x - split * tiles;
-    const int64_t tile = (int64_t)c.expert * tiles + t, row = tile * 64 + lane;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int tiles = hidden >> 6, part = w & (parts - 1), t = blockIdx.x * (kDefaultWaves / parts) + w / parts;
+    const bool owns = t < tiles; // the last workgroup may have waves too many
+    const int64_t tile = (int64_t)c.expert * tiles + min(t, tiles - 1);
     auto pair_of = [&](int j) { return (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8); };
+    float *out = partial + blockIdx.z * pairs * hidden + t * 64 + lane;
     float sum[4 * NQ];
-    const int workers = waves * splits, worker = split * waves + w;
-    tile_product<BITS, NQ>(down, tile, row, inter >> 8, worker, inter >> 7, workers, worker, workers, 4 * NQ,
-                           [&](int j) { return a + ((j >= T ? pairs : 0) + pair_of(min(j % T, c.count - 1))) * inter; }, sum);
+    const int workers = parts * gridDim.z, worker = blockIdx.z * parts + part;
+    if (owns)
+        tile_product<BITS, NQ, T>(
+            down, tile, inter >> 8, worker, workers, c.count,
+            [&](int j) { return (j < T ? a.hi : a.lo) + pair_of(min(j & (T - 1), c.count - 1)) * inter; },
+            [&](int j, int col) { return a.whole[pair_of(j) * inter + col]; }, sum);
+    if (parts == 1) {
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            if (owns && j < c.count) out[pair_of(j) * hidden] = sum[j] + sum[T + j];
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < T; ++j) red[(w * T + j) * 64 + lane] = sum[j] + sum[T + j];
     __syncthreads();
-    for (int j = w; j < c.count; j += waves) {
+    const int w0 = w - part;
+    for (int j = part; j < c.count; j += parts) {
         float v = 0.f;
-        for (int k = 0; k < waves; ++k) v += red[(k * T + j) * 64 + lane];
-        part[((int64_t)split * pairs + pair_of(j)) * hidden + t * 64 + lane] = v;
+        for (int k = w0; k < w0 + parts; ++k) v += red[(k * T + j) * 64 + lane];
+        if (owns) out[pair_of(j) * hidden] = v;
     }
 }
 
 template <int BITS, int MAXQ>
-__global__ void __launch_bounds__(kMaxWaves * 64) experts_down(Projection down, const uint16_t *a, const int32_t *ids,
-                                                               int batch, int experts, int topk, int hidden, int inter,
-                                                               int splits, float *part)
+__global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down(Projection down, Activations a,
+                                                                      const int32_t *ids, int batch, int experts,
+                                                                      int topk, int hidden, int inter, int parts,
+                                                                      float *partial)
 {
-    __shared__ ChosenLds chosen[kMaxWaves];
+    __shared__ ChosenLds chosen[kDefaultWaves];
     extern __shared__ float red[];
     ChosenLds &lds = chosen[threadIdx.x >> 6];
     const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
     if (c.expert < 0) return;
     const int64_t pairs = batch * topk;
     if (MAXQ >= 4 && c.count > 8)
-        down_body<BITS, MAXQ >= 4 ? 8 : 2>(down, a, lds, c, topk, hidden, inter, splits, pairs, part, red);
+        down_body<BITS, MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
     else if (MAXQ >= 2 && c.count > 4)
-        down_body<BITS, MAXQ >= 2 ? 4 : 2>(down, a, lds, c, topk, hidden, inter, splits, pairs, part, red);
+        down_body<BITS, MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
+    else if (MAXQ >= 1 && c.count > 2)
+        down_body<BITS, MAXQ >= 1 ? 2 : 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
     else
-        down_body<BITS, 2>(down, a, lds, c, topk, hidden, inter, splits, pairs, part, red);
+        down_body<BITS, 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
 }
 
 // y = the weighted sum of a token's partial sums, in the order of its choices;
@@ -548,6 +624,19 @@ sqllm_status check_sizes(int batch, int experts, int topk, int64_t hidden, int64
 
 int64_t used_at_most(int batch, int experts, int topk) { return batch * topk < experts ? batch * topk : experts; }
 
+// Waves per tile (8 to a workgroup).  A wave alone on a tile spends least on
+// finding its expert, its table and the sums between waves, but enough waves
+// have to be in flight to keep the memory busy: about kWavesWanted over the
+// 256 compute units.
+constexpr int64_t kWavesWanted = 256 * 16;
+
+int parts_for(int64_t tiles, int least)
+{
+    int p = least;
+    while (p < kDefaultWaves && tiles * p < kWavesWanted) p *= 2;
+    return p;
+}
+
 // Workgroups that share a down tile's columns: more than one only while the
 // launch would leave compute units without work and every wave keeps at
 // least two half groups.
@@ -567,7 +656,7 @@ struct Layout {
         const size_t pairs = (size_t)batch * topk;
         logits = 0;
         act = up((size_t)batch * experts * 8);
-        part = act + up(pairs * inter * 4);
+        part = act + up(pairs * inter * 8);
         end = part + up(pairs * hidden * 4 * down_splits(batch, experts, topk, hidden, inter));
     }
 };
@@ -633,15 +722,20 @@ sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weight
                       const Projection &up, const Projection &down, int batch, int experts, int topk, int hidden,
                       int inter, uint16_t *y, const Layout &at, char *ws, hipStream_t stream)
 {
-    uint16_t *a = (uint16_t *)(ws + at.act);
+    const size_t entries = (size_t)batch * topk * inter;
+    const Activations a = {(uint16_t *)(ws + at.act), (uint16_t *)(ws + at.act) + entries,
+                           (float *)(ws + at.act + 4 * entries)};
     float *part = (float *)(ws + at.part);
     const int used = (int)used_at_most(batch, experts, topk), splits = down_splits(batch, experts, topk, hidden, inter);
-    const int waves = kDefaultWaves;
-    const size_t red = (size_t)waves * 4 * MAXQ * 64 * sizeof(float);
-    hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(inter / 64, used), dim3(64 * waves), red, stream, gate, up, x,
-                       ids, batch, experts, topk, hidden, inter, a);
-    hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(hidden / 64 * splits, used), dim3(64 * waves), red, stream, down,
-                       a, ids, batch, experts, topk, hidden, inter, splits, part);
+    const size_t red = (size_t)kDefaultWaves * 4 * MAXQ * 64 * sizeof(float);
+    const int gate_parts = parts_for((int64_t)used * (inter / 64), 2);
+    const int down_parts = parts_for((int64_t)used * (hidden / 64) * splits, 1);
+    auto wgs = [](int tiles, int parts) { return (tiles * parts + kDefaultWaves - 1) / kDefaultWaves; };
+    hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(wgs(inter / 64, gate_parts), used), dim3(64 * kDefaultWaves),
+                       red, stream, gate, up, x, ids, batch, experts, topk, hidden, inter, gate_parts, a);
+    hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(wgs(hidden / 64, down_parts), used, splits),
+                       dim3(64 * kDefaultWaves), red, stream, down, a, ids, batch, experts, topk, hidden, inter,
+                       down_parts, part);
     hipLaunchKernelGGL(experts_combine, dim3(hidden / 256, batch), dim3(256), 0, stream, part, ids, weights, batch,
                        experts, topk, hidden, splits, y);
     return launched();

@@ -26,19 +26,45 @@ constexpr int64_t kMaxWidth = 65536; // hidden, inter: 16-bit columns of the out
 // Router.
 // ---------------------------------------------------------------------------
 
-// logits[t][e], one wave each, in 64 bits: a product of two fp16 values is
-// exact in fp32, and 64-bit sums of at most 2^16 of them are off by less
-// than 2^-37 of the largest partial sum, so the choice below does not
-// depend on the order they are taken in.
-__global__ void __launch_bounds__(64) route_logits(const uint16_t *__restrict__ x, const uint16_t *__restrict__ router,
-                                                   int hidden, int experts, double *__restrict__ logits)
+// Sums in 64 bits: a product of two fp16 values is exact in fp32, and 64-bit
+// sums of at most 2^16 of them are off by less than 2^-37 of the largest
+// partial sum, so the choice does not depend on the order they are taken in.
+
+typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+
+// This lane's part of the sums of R router rows with T tokens' x: 16 bytes of
+// each per 512 columns (hidden is a multiple of 256: the last 512 may be half
+// there).
+template <int R, int T>
+__device__ __forceinline__ void row_sums(const uint16_t *const (&w)[R], const uint16_t *const (&x)[T], int hidden,
+                                         int lane, double (&sum)[R][T])
 {
-    const int e = blockIdx.x, t = blockIdx.y, lane = threadIdx.x;
-    const _Float16 *xr = (const _Float16 *)x + (int64_t)t * hidden, *wr = (const _Float16 *)router + (int64_t)e * hidden;
-    double acc = 0.0;
-    for (int c = lane; c < hidden; c += 64) acc += (double)((float)xr[c] * (float)wr[c]);
-    for (int m = 32; m; m >>= 1) acc += __shfl_xor(acc, m);
-    if (lane == 0) logits[(int64_t)t * experts + e] = acc;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < T; ++t) sum[r][t] = 0.0;
+#pragma unroll(R * T > 1 ? 2 : 4)
+    for (int c = lane * 8; c < hidden; c += 512) {
+        half8_t wv[R], xv[T];
+#pragma unroll
+        for (int r = 0; r < R; ++r) wv[r] = *(const half8_t *)(w[r] + c);
+#pragma unroll
+        for (int t = 0; t < T; ++t) xv[t] = *(const half8_t *)(x[t] + c);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[r][t] += (double)((float)wv[r][i] * (float)xv[t][i]);
+    }
+}
+
+// The sum over the wave's lanes, in every lane.
+__device__ __forceinline__ double wave_sum(double v)
+{
+#pragma unroll
+    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+    return v;
 }
 
 // A double's place in ascending order as an unsigned number; NaN is 0, below
@@ -50,75 +76,154 @@ __device__ __forceinline__ uint64_t order_key(double v)
     return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
 
-// One wave per token; lane l holds experts l, l + 64, ...  Each of the topk
-// rounds takes the largest key left (ties: the lowest expert).
-__global__ void __launch_bounds__(64) route_select(const double *__restrict__ logits, const float *__restrict__ bias,
-                                                   int experts, int topk, int flags, float scale,
-                                                   int32_t *__restrict__ ids, float *__restrict__ weights)
+// The largest v of the wave, in every lane: DPP shifts within rows of 16 and
+// broadcasts across them leave it in lane 63.
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-    constexpr int N = kMaxExperts / 64;
-    const int t = blockIdx.x, lane = threadIdx.x;
+#define SQLLM_MAX_STEP(ctrl, rows) v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, true))
+    SQLLM_MAX_STEP(0x111, 0xF); // row_shr 1, 2, 4, 8
+    SQLLM_MAX_STEP(0x112, 0xF);
+    SQLLM_MAX_STEP(0x114, 0xF);
+    SQLLM_MAX_STEP(0x118, 0xF);
+    SQLLM_MAX_STEP(0x142, 0xA); // row_bcast 15, 31
+    SQLLM_MAX_STEP(0x143, 0xC);
+#undef SQLLM_MAX_STEP
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
+// One wave's choice for one token; lane l holds experts l, l + 64, ... (N of
+// them; logit(e) is expert e's sum).  Each of the topk rounds takes the
+// largest key left, by its upper and then its lower half (ties: the lowest
+// expert).
+template <int N, typename L>
+__device__ __forceinline__ void choose(L logit, const float *bias, int experts, int topk, int flags, float scale,
+                                       int32_t *ids, float *weights)
+{
+    const int lane = threadIdx.x & 63;
     double s[N];
     uint64_t key[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) s[j] = lane + 64 * j < experts ? logit(lane + 64 * j) : -__builtin_inf();
     if (flags & SQLLM_MOE_SIGMOID) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int e = lane + 64 * j;
-            s[j] = e < experts ? 1.0 / (1.0 + exp(-logits[(int64_t)t * experts + e])) : 0.0;
-        }
+        for (int j = 0; j < N; ++j) s[j] = 1.0 / (1.0 + exp(-s[j]));
     } else {
-        double top = -__builtin_inf(), sum = 0.0;
+        double top = s[0], sum = 0.0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int e = lane + 64 * j;
-            s[j] = e < experts ? logits[(int64_t)t * experts + e] : -__builtin_inf();
-            top = fmax(top, s[j]);
-        }
+        for (int j = 1; j < N; ++j) top = fmax(top, s[j]);
+#pragma unroll
         for (int m = 32; m; m >>= 1) top = fmax(top, __shfl_xor(top, m));
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             s[j] = lane + 64 * j < experts ? exp(s[j] - top) : 0.0;
             sum += s[j];
         }
-        for (int m = 32; m; m >>= 1) sum += __shfl_xor(sum, m);
+        sum = wave_sum(sum);
 #pragma unroll
         for (int j = 0; j < N; ++j) s[j] /= sum;
     }
+    // bit j of left: expert lane + 64 j can still be chosen
+    uint32_t left = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
         const int e = lane + 64 * j;
+        if (e < experts) left |= 1u << j;
         key[j] = e < experts ? order_key(bias ? s[j] + (double)bias[e] : s[j]) : 0;
     }
-    int taken = 0; // bit j: this lane's expert j is chosen already
-    double kept[kMaxTopk], sum = 0.0;
+    double kept = 0.0, sum = 0.0; // lane k ends with the k-th score
+    int mine = 0;
     for (int k = 0; k < topk; ++k) {
         uint64_t best = 0;
-        int at = INT32_MAX;
+        int at = -1;
         double sc = 0.0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int e = lane + 64 * j;
-            if (e < experts && !((taken >> j) & 1) && (at == INT32_MAX || key[j] > best)) best = key[j], at = e, sc = s[j];
+        for (int j = 0; j < N; ++j)
+            if (((left >> j) & 1) && (at < 0 || key[j] > best)) best = key[j], at = j, sc = s[j];
+        uint64_t with = __ballot(at >= 0);
+        const uint32_t hi = wave_max(at >= 0 ? (uint32_t)(best >> 32) : 0);
+        with &= __ballot((uint32_t)(best >> 32) == hi);
+        if (with & (with - 1)) { // several: the lower half decides, then the lowest expert
+            const bool in = (with >> lane) & 1;
+            const uint32_t lo = wave_max(in ? (uint32_t)best : 0);
+            with &= __ballot((uint32_t)best == lo);
+            if (with & (with - 1)) {
+                const uint32_t first = ~wave_max((with >> lane) & 1 ? ~(uint32_t)(lane + 64 * at) : 0);
+                with = 1ull << (first & 63);
+            }
         }
-        for (int m = 32; m; m >>= 1) {
-            const uint64_t ob = __shfl_xor((unsigned long long)best, m);
-            const int oa = __shfl_xor(at, m);
-            const double os = __shfl_xor(sc, m);
-            if (oa != INT32_MAX && (at == INT32_MAX || ob > best || (ob == best && oa < at))) best = ob, at = oa, sc = os;
-        }
-        if ((at & 63) == lane) taken |= 1 << (at >> 6);
-#pragma unroll
-        for (int q = 0; q < kMaxTopk; ++q)
-            if (q == k) kept[q] = sc;
-        sum += sc;
-        if (lane == 0) ids[t * topk + k] = at;
+        const int owner = __builtin_ctzll(with), e = owner + 64 * __builtin_amdgcn_readlane(at, owner);
+        const double got = __shfl(sc, owner);
+        if (lane == owner) left &= ~(1u << at);
+        if (lane == k) kept = got, mine = e;
+        sum += got;
     }
-    if (lane == 0) {
-        const double f = flags & SQLLM_MOE_KEEP_SUM ? (double)scale : (double)scale / sum;
-#pragma unroll
-        for (int k = 0; k < kMaxTopk; ++k)
-            if (k < topk) weights[t * topk + k] = (float)(kept[k] * f);
+    if (lane < topk) {
+        ids[lane] = mine;
+        weights[lane] = (float)(kept * (flags & SQLLM_MOE_KEEP_SUM ? (double)scale : (double)scale / sum));
     }
+}
+
+// Small routers in one launch: a workgroup of sixteen waves does all of one
+// token.
+constexpr int kRouteWaves = 16;
+
+template <int N>
+__global__ void __launch_bounds__(64 * kRouteWaves) route_small(const uint16_t *__restrict__ x,
+                                                                const uint16_t *__restrict__ router,
+                                                                const float *__restrict__ bias, int hidden, int experts,
+                                                                int topk, int flags, float scale,
+                                                                int32_t *__restrict__ ids, float *__restrict__ weights)
+{
+    __shared__ double logits[64 * N];
+    const int t = blockIdx.x, w = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const uint16_t *const xt[1] = {x + (int64_t)t * hidden};
+    constexpr int R = 4; // rows at a time, so that their loads and sums over the wave overlap
+    for (int e = w * R; e < experts; e += kRouteWaves * R) {
+        const uint16_t *row[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) row[r] = router + (int64_t)min(e + r, experts - 1) * hidden;
+        double sum[R][1];
+        row_sums(row, xt, hidden, lane, sum);
+#pragma unroll
+        for (int r = 0; r < R; ++r) sum[r][0] = wave_sum(sum[r][0]);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (lane == 0 && e + r < experts) logits[e + r] = sum[r][0];
+    }
+    __syncthreads();
+    if (w == 0)
+        choose<N>([&](int e) { return logits[e]; }, bias, experts, topk, flags, scale, ids + t * topk, weights + t * topk);
+}
+
+// Larger ones in two: logits[t][e], a wave for one expert and T tokens, then
+// the choice.
+template <int T>
+__global__ void __launch_bounds__(256) route_logits(const uint16_t *__restrict__ x, const uint16_t *__restrict__ router,
+                                                    int hidden, int experts, int batch, double *__restrict__ logits)
+{
+    const int e = blockIdx.x * 4 + (threadIdx.x >> 6), t0 = blockIdx.y * T, lane = threadIdx.x & 63;
+    if (e >= experts) return;
+    const uint16_t *xt[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) xt[t] = x + (int64_t)min(t0 + t, batch - 1) * hidden;
+    const uint16_t *const row[1] = {router + (int64_t)e * hidden};
+    double sum[1][T];
+    row_sums(row, xt, hidden, lane, sum);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const double v = wave_sum(sum[0][t]);
+        if (lane == 0 && t0 + t < batch) logits[(int64_t)(t0 + t) * experts + e] = v;
+    }
+}
+
+template <int N>
+__global__ void __launch_bounds__(64) route_choose(const double *__restrict__ logits, const float *__restrict__ bias,
+                                                   int experts, int topk, int flags, float scale,
+                                                   int32_t *__restrict__ ids, float *__restrict__ weights)
+{
+    const int t = blockIdx.x;
+    choose<N>([&](int e) { return logits[(int64_t)t * experts + e]; }, bias, experts, topk, flags, scale, ids + t * topk,
+              weights + t * topk);
 }
 
 // ---------------------------------------------------------------------------
@@ -252,24 +357,35 @@ struct Half {
     }
 };
 
-// A half group's activations of a quad of tokens: lane 4n + i holds token i's
-// values of steps 2n (x, y) and 2n + 1 (z, w) in the order above.
+// A half group's activations of a quad of tokens: lane 4n + i loads what
+// token i has for steps 2n and 2n + 1 (at 2 bits the two lane blocks of 16
+// columns load all of them), put into the order above when it is used.
 template <int BITS>
-__device__ __forceinline__ u32x4 step_order(const uint16_t *x, int block) // x: the token's 128 columns
-{
-    if constexpr (BITS == 2) {
-        const u32x4 *p = (const u32x4 *)(x + 16 * (block >> 1));
-        const u32x4 a = p[0], b = p[1];
-        const bool odd = block & 1; // columns 2, 3 of each four instead of 0, 1
-        const uint32_t a0 = odd ? a.y : a.x, a1 = odd ? a.w : a.z, b0 = odd ? b.y : b.x, b1 = odd ? b.w : b.z;
+struct QuadX {
+    u32x4 raw[BITS == 2 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const uint16_t *x, int block) // x: the token's 128 columns
+    {
+        if constexpr (BITS == 2) {
+            const u32x4 *p = (const u32x4 *)(x + 16 * (block >> 1));
+            raw[0] = p[0], raw[1] = p[1];
+        } else {
+            raw[0] = *(const u32x4 *)(x + 8 * block);
+        }
+    }
+
+    __device__ __forceinline__ u32x4 ordered(int block) const // x, y: step 2n; z, w: step 2n + 1
+    {
+        uint32_t a0 = raw[0].x, a1 = raw[0].y, b0 = raw[0].z, b1 = raw[0].w;
+        if constexpr (BITS == 2) {
+            const bool odd = block & 1; // columns 2, 3 of each four instead of 0, 1
+            a0 = odd ? raw[0].y : raw[0].x, a1 = odd ? raw[0].w : raw[0].z;
+            b0 = odd ? raw[1].y : raw[1].x, b1 = odd ? raw[1].w : raw[1].z;
+        }
         return u32x4{perm(a1, a0, 0x05040100), perm(b1, b0, 0x05040100), perm(a1, a0, 0x07060302),
                      perm(b1, b0, 0x07060302)};
-    } else {
-        const u32x4 v = *(const u32x4 *)(x + 8 * block);
-        return u32x4{perm(v.y, v.x, 0x05040100), perm(v.w, v.z, 0x05040100), perm(v.y, v.x, 0x07060302),
-                     perm(v.w, v.z, 0x07060302)};
     }
-}
+};
 
 // The experts in use, each once and in ascending order, are the launch's grid
 // rows: which expert row `slot` is, and which tokens chose it.  Every wave
@@ -357,67 +473,79 @@ __device__ __forceinline__ void add_chunk(uint32_t val, float x, int cb, int v1,
 // token j at column c in fp32, for the outliers of tokens below `tokens`.
 // Column 4h + i of the matrix steps ends in sum[4h + i]; an outlier of token j
 // is added to sum[j].
-template <int BITS, int NQ>
-struct Accumulators {
-    f32x4 even[NQ], odd[NQ]; // two chains, so that a matrix step does not wait for the one before it
-};
-
 template <int BITS, int NQ, int T, typename X, typename V>
 __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int groups, int worker, int workers,
                                              int tokens, X x, V value, float (&sum)[4 * NQ])
 {
-    constexpr int D = NQ <= 2 ? 3 : (NQ <= 4 ? 2 : 1); // half groups in flight
-    const int lane = threadIdx.x & 63, block = lane >> 2, end = 2 * groups;
+    // half groups in flight, as many as fit 128 registers without spilling
+    constexpr int D = NQ == 1 ? (BITS == 2 ? 3 : 4) : (NQ == 2 ? (BITS == 2 ? 2 : 3) : (NQ == 4 && BITS == 3 ? 2 : 1));
+    constexpr int C = NQ == 1 ? 2 : 1; // accumulator chains: a step does not wait for the one before it
+    const int lane = threadIdx.x & 63, block = lane >> 2;
     const int64_t row = tile * 64 + lane;
     Table<BITS> table;
     table.load(p.lut + (row << BITS));
     int rp_lo = 0, rp_hi = 0;
     if (p.nnz) rp_lo = p.row_ptr[row], rp_hi = p.row_ptr[row + 1];
-    const uint8_t *codes = p.packed + tile * groups * (2 * BITS * 1024) + lane * 16;
+    const int n = max(0, (2 * groups - worker + workers - 1) / workers); // half groups of this wave
+    const uint8_t *codes = p.packed + tile * groups * (2 * BITS * 1024);
     const uint16_t *xr[NQ];
 #pragma unroll
     for (int h = 0; h < NQ; ++h) xr[h] = x(4 * h + (lane & 3));
     Half<BITS> ring[D];
-    u32x4 xq[D][NQ];
-    auto load = [&](int k, int g) {
-        ring[k].load(codes + (int64_t)g * (BITS * 1024));
+    QuadX<BITS> xq[D][NQ];
+    // The same loads in every step, so that the waits before a step leave the
+    // ring's other loads in flight: past the wave's last half group they read
+    // a few cached zeros.
+    auto load = [&](int k, int i) {
+        const int g = worker + i * workers;
+        ring[k].load((i < n ? codes + (int64_t)g * (BITS * 1024) : (const uint8_t *)dev::g_placeholder) + lane * 16);
 #pragma unroll
-        for (int h = 0; h < NQ; ++h) xq[k][h] = step_order<BITS>(xr[h] + 128 * g, block);
+        for (int h = 0; h < NQ; ++h)
+            xq[k][h].load(i < n ? xr[h] + 128 * g : (const uint16_t *)dev::g_placeholder, block);
     };
-    Accumulators<BITS, NQ> acc;
+    f32x4 acc[NQ][C];
 #pragma unroll
-    for (int h = 0; h < NQ; ++h) acc.even[h] = acc.odd[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int h = 0; h < NQ; ++h)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[h][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto multiply = [&](int k) {
+        u32x4 xs[NQ];
+#pragma unroll
+        for (int h = 0; h < NQ; ++h) xs[h] = xq[k][h].ordered(block);
         [&]<int... Ns>(std::integer_sequence<int, Ns...>) {
             (
                 [&] {
                     const half4_t we = ring[k].template weights<2 * Ns>(table);
                     const half4_t wo = ring[k].template weights<2 * Ns + 1>(table);
 #pragma unroll
-                    for (int h = 0; h < NQ; ++h) {
-                        const half4_t xe = __builtin_bit_cast(half4_t, u32x2{xq[k][h].x, xq[k][h].y});
-                        const half4_t xo = __builtin_bit_cast(half4_t, u32x2{xq[k][h].z, xq[k][h].w});
-                        acc.even[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(xe, we, acc.even[h], 4, Ns, 0);
-                        acc.odd[h] = __builtin_amdgcn_mfma_f32_4x4x4f16(xo, wo, acc.odd[h], 4, Ns, 0);
-                    }
+                    for (int h = 0; h < NQ; ++h)
+                        acc[h][0] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2{xs[h].x, xs[h].y}),
+                                                                      we, acc[h][0], 4, Ns, 0);
+#pragma unroll
+                    for (int h = 0; h < NQ; ++h)
+                        acc[h][C - 1] = __builtin_amdgcn_mfma_f32_4x4x4f16(
+                            __builtin_bit_cast(half4_t, u32x2{xs[h].z, xs[h].w}), wo, acc[h][C - 1], 4, Ns, 0);
                 }(),
                 ...);
         }(std::make_integer_sequence<int, 16>{});
     };
 #pragma unroll
-    for (int k = 0; k < D; ++k)
-        if (worker + k * workers < end) load(k, worker + k * workers);
-    for (int g = worker; g < end; g += D * workers) {
+    for (int k = 0; k < D; ++k) load(k, k);
+    int i = 0;
+    for (; i + D <= n; i += D) {
 #pragma unroll
         for (int k = 0; k < D; ++k) {
-            if (g + k * workers < end) multiply(k);
-            if (g + (k + D) * workers < end) load(k, g + (k + D) * workers);
+            multiply(k);
+            load(k, i + k + D);
         }
     }
 #pragma unroll
+    for (int k = 0; k < D - 1; ++k)
+        if (i + k < n) multiply(k);
+#pragma unroll
     for (int h = 0; h < NQ; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[4 * h + i] = acc.even[h][i] + acc.odd[h][i];
+        for (int r = 0; r < 4; ++r) sum[4 * h + r] = C == 2 ? acc[h][0][r] + acc[h][C - 1][r] : acc[h][0][r];
     // outliers: a nonzero per lane, kChunks of 64 at a time so that a round
     // waits for memory twice; a prefix sum over the wave gives every row's
     // run of products as a difference
@@ -454,9 +582,11 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
 // a = silu(gate x) * (up x), split into two fp16 values per entry for the
 // matrix steps of down (storing a in one would double the error of y) and
 // whole for its outliers.
-// `parts` waves share a tile, the even ones gate and the odd ones up; the
-// eight waves of a workgroup have neighbouring tiles of one expert.
-// Grid (inter / 64 / (8 / parts), experts in use at most).
+// The even waves of a workgroup have the gate's tile, the odd ones the up's.
+// (Two or four tiles to a workgroup, with two or four of its waves each,
+// measured no faster anywhere: 16 tokens, 128 experts 1536x4096 103 and 92 us
+// against 90; one token, 6 experts 1280x2048 22 and 14 us against 10.)
+// Grid (inter / 64, experts in use at most).
 // ---------------------------------------------------------------------------
 struct Activations { // [pair][inter]
     uint16_t *hi, *lo;
@@ -466,24 +596,24 @@ struct Activations { // [pair][inter]
 template <int BITS, int NQ>
 __device__ __forceinline__ void gate_up_body(const Projection &gate, const Projection &up, const uint16_t *x,
                                              const ChosenLds &lds, Chosen c, int topk, int hidden, int inter,
-                                             int parts, Activations a, float *red)
+                                             Activations a, float *red)
 {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int part = w & (parts - 1), t = blockIdx.x * (kDefaultWaves / parts) + w / parts;
+    const int t = blockIdx.x;
     const int64_t tile = (int64_t)c.expert * (inter >> 6) + t;
     auto row_of = [&](int j) { return x + (int64_t)(lds.list[j] & 255) * hidden; };
     float sum[4 * NQ];
     tile_product<BITS, NQ, 4 * NQ>(
-        part & 1 ? up : gate, tile, hidden >> 8, part >> 1, parts >> 1, c.count,
+        w & 1 ? up : gate, tile, hidden >> 8, w >> 1, kDefaultWaves / 2, c.count,
         [&](int j) { return row_of(min(j, c.count - 1)); }, // past the last: a copy, whose sums are dropped
         [&](int j, int col) { return dev::f16_to_f32(row_of(j)[col]); }, sum);
 #pragma unroll
     for (int j = 0; j < 4 * NQ; ++j) red[(w * 4 * NQ + j) * 64 + lane] = sum[j];
     __syncthreads();
-    const int w0 = w - part;
-    for (int j = part; j < c.count; j += parts) {
+    for (int j = w; j < c.count; j += kDefaultWaves) {
         float g = 0.f, u = 0.f;
-        for (int k = w0; k < w0 + parts; k += 2) {
+#pragma unroll
+        for (int k = 0; k < kDefaultWaves; k += 2) {
             g += red[(k * 4 * NQ + j) * 64 + lane];
             u += red[((k + 1) * 4 * NQ + j) * 64 + lane];
         }
@@ -501,7 +631,7 @@ __device__ __forceinline__ void gate_up_body(const Projection &gate, const Proje
 template <int BITS, int MAXQ>
 __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Projection gate, Projection up, const uint16_t *x,
                                                                   const int32_t *ids, int batch, int experts, int topk,
-                                                                  int hidden, int inter, int parts, Activations a)
+                                                                  int hidden, int inter, Activations a)
 {
     __shared__ ChosenLds chosen[kDefaultWaves];
     extern __shared__ float red[];
@@ -509,17 +639,17 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Project
     const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
     if (c.expert < 0) return;
     if (MAXQ >= 4 && c.count > 8)
-        gate_up_body<BITS, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, parts, a, red);
+        gate_up_body<BITS, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, a, red);
     else if (MAXQ >= 2 && c.count > 4)
-        gate_up_body<BITS, MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, parts, a, red);
+        gate_up_body<BITS, MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, a, red);
     else
-        gate_up_body<BITS, 1>(gate, up, x, lds, c, topk, hidden, inter, parts, a, red);
+        gate_up_body<BITS, 1>(gate, up, x, lds, c, topk, hidden, inter, a, red);
 }
 
 // ---------------------------------------------------------------------------
 // part[split][pair][hidden] = down a, fp32, over the split's columns.  A
 // token j's two fp16 values stand in columns j and 2 NQ + j.  `parts` waves
-// share a tile and split, as above.
+// share a tile and split.
 // Grid (ceil(hidden / 64 / (8 / parts)), experts in use at most, splits).
 // ---------------------------------------------------------------------------
 template <int BITS, int NQ>
@@ -624,16 +754,17 @@ sqllm_status check_sizes(int batch, int experts, int topk, int64_t hidden, int64
 
 int64_t used_at_most(int batch, int experts, int topk) { return batch * topk < experts ? batch * topk : experts; }
 
-// Waves per tile (8 to a workgroup).  A wave alone on a tile spends least on
-// finding its expert, its table and the sums between waves, but enough waves
-// have to be in flight to keep the memory busy: about kWavesWanted over the
-// 256 compute units.
-constexpr int64_t kWavesWanted = 256 * 16;
-
-int parts_for(int64_t tiles, int least)
+// Waves that share a down tile (8 waves to a workgroup): all eight while the
+// launch then fits the compute units at once (20 waves each).  Beyond that a
+// wave keeps at least three half groups, since finding its expert, its table
+// and the sums between waves cost it as much as three (16 tokens, 128 experts
+// 4096x1536: 82 us at eight waves, 61 at four, 60 at two, 67 at one; 8
+// experts 4096x3584: 27, 31, 49 and 88 us).
+int down_parts_for(int64_t tiles, int64_t inter)
 {
-    int p = least;
-    while (p < kDefaultWaves && tiles * p < kWavesWanted) p *= 2;
+    int p = kDefaultWaves;
+    if (tiles * p > 256 * 20)
+        while (p > 1 && inter / 128 < 3 * p) p /= 2;
     return p;
 }
 
@@ -699,16 +830,30 @@ sqllm_status check_products(const uint16_t *x, const int32_t *ids, const float *
     return SQLLM_OK;
 }
 
+constexpr int64_t kRouteSmall = 131072; // experts * hidden up to which one launch routes
+
 sqllm_status launched() { return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP; }
 
 sqllm_status route(const uint16_t *x, const uint16_t *router, const float *bias, int batch, int experts,
                    int64_t hidden, int topk, int flags, float scale, int32_t *ids, float *weights, const Layout &at,
                    char *ws, hipStream_t stream)
 {
+    const int n = (experts + 63) / 64; // experts per lane of the choosing wave
+    if ((int64_t)experts * hidden <= kRouteSmall) {
+        auto kern = n == 1 ? route_small<1> : n == 2 ? route_small<2> : n <= 4 ? route_small<4> : route_small<8>;
+        hipLaunchKernelGGL(kern, dim3(batch), dim3(64 * kRouteWaves), 0, stream, x, router, bias, (int)hidden, experts,
+                           topk, flags, scale, ids, weights);
+        return launched();
+    }
     double *logits = (double *)(ws + at.logits);
-    hipLaunchKernelGGL(route_logits, dim3(experts, batch), dim3(64), 0, stream, x, router, (int)hidden, experts, logits);
-    hipLaunchKernelGGL(route_select, dim3(batch), dim3(64), 0, stream, logits, bias, experts, topk, flags, scale, ids,
-                       weights);
+    if (batch == 1)
+        hipLaunchKernelGGL((route_logits<1>), dim3((experts + 3) / 4, 1), dim3(256), 0, stream, x, router, (int)hidden,
+                           experts, batch, logits);
+    else
+        hipLaunchKernelGGL((route_logits<2>), dim3((experts + 3) / 4, (batch + 1) / 2), dim3(256), 0, stream, x, router,
+                           (int)hidden, experts, batch, logits);
+    auto kern = n == 1 ? route_choose<1> : n == 2 ? route_choose<2> : n <= 4 ? route_choose<4> : route_choose<8>;
+    hipLaunchKernelGGL(kern, dim3(batch), dim3(64), 0, stream, logits, bias, experts, topk, flags, scale, ids, weights);
     return launched();
 }
 
@@ -728,12 +873,11 @@ sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weight
     float *part = (float *)(ws + at.part);
     const int used = (int)used_at_most(batch, experts, topk), splits = down_splits(batch, experts, topk, hidden, inter);
     const size_t red = (size_t)kDefaultWaves * 4 * MAXQ * 64 * sizeof(float);
-    const int gate_parts = parts_for((int64_t)used * (inter / 64), 2);
-    const int down_parts = parts_for((int64_t)used * (hidden / 64) * splits, 1);
-    auto wgs = [](int tiles, int parts) { return (tiles * parts + kDefaultWaves - 1) / kDefaultWaves; };
-    hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(wgs(inter / 64, gate_parts), used), dim3(64 * kDefaultWaves),
-                       red, stream, gate, up, x, ids, batch, experts, topk, hidden, inter, gate_parts, a);
-    hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(wgs(hidden / 64, down_parts), used, splits),
+    const int down_parts = down_parts_for((int64_t)used * (hidden / 64) * splits, inter / splits);
+    const int down_wgs = (hidden / 64 * down_parts + kDefaultWaves - 1) / kDefaultWaves;
+    hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(inter / 64, used), dim3(64 * kDefaultWaves),
+                       red, stream, gate, up, x, ids, batch, experts, topk, hidden, inter, a);
+    hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(down_wgs, used, splits),
                        dim3(64 * kDefaultWaves), red, stream, down, a, ids, batch, experts, topk, hidden, inter,
                        down_parts, part);
     hipLaunchKernelGGL(experts_combine, dim3(hidden / 256, batch), dim3(256), 0, stream, part, ids, weights, batch,

@@ -6,10 +6,11 @@ activations to the same form and runs on the matrix cores, at any batch."""
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from . import _calls, _check, _dev, _lib
+from . import _calls, _check, _lib
 
 _vp, _i64, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _lib.sqllm_fp8_cols.restype = _i64
@@ -27,70 +28,61 @@ EXPORTS = ("sqllm_fp8_cols", "sqllm_fp8_scale_pitch", "sqllm_fp8_quantize", "sql
            "sqllm_fp8_gemm")
 
 
+@functools.lru_cache(maxsize=4096)
 def fp8_cols(cols: int) -> int:
     """Columns of the stored codes: cols rounded up to 128 (0 if out of range)."""
     return int(_lib.sqllm_fp8_cols(cols))
 
 
+@functools.lru_cache(maxsize=4096)
 def fp8_scale_pitch(cols: int) -> int:
     """Bytes of a row of scales: one per block of 128 columns, rounded up to 4 (0 if out of range)."""
     return int(_lib.sqllm_fp8_scale_pitch(cols))
 
 
+@functools.lru_cache(maxsize=4096)
 def fp8_workspace_bytes(rows: int, cols: int, batch: int) -> int:
     return int(_lib.sqllm_fp8_workspace_bytes(rows, cols, batch))
 
 
-def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, stream=None):
+@_calls.on_stream
+def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, *, index, handle):
     """(q, scale) of fp16 x [rows, cols]; the columns of a row are adjacent, rows may be further apart than cols.
-    Offline for weights; the product rounds its activations itself."""
-    dev = _calls.one_device((("x", x), ("q", q), ("scale", scale)))
+    Offline for weights; the product rounds its activations itself.  stream: as for every call (keyword)."""
     if x.dim() != 2 or x.numel() == 0:
         raise ValueError(f"x: shape (rows, cols) expected, got {tuple(x.shape)}")
-    if x.dtype != torch.float16:
+    if x.dtype is not torch.float16:
         raise TypeError(f"x: dtype torch.float16 expected, got {x.dtype}")
     rows, cols = x.shape
     if cols > 1 and x.stride(1) != 1:
         raise ValueError("x: adjacent columns expected")
-    ldx = x.stride(0) if rows > 1 else cols
-    with _calls.on(dev, stream):
-        shapes = (rows, fp8_cols(cols)), (rows, fp8_scale_pitch(cols))
-        q = torch.empty(shapes[0], dtype=torch.uint8, device=dev) if q is None else q
-        scale = torch.empty(shapes[1], dtype=torch.uint8, device=dev) if scale is None else scale
-        for name, t, shape in (("q", q, shapes[0]), ("scale", scale, shapes[1])):
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
-        _check(_lib.sqllm_fp8_quantize(x.data_ptr(), rows, cols, ldx, _dev(q, "q", torch.uint8),
-                                       _dev(scale, "scale", torch.uint8), torch.cuda.current_stream().cuda_stream),
-               "sqllm_fp8_quantize")
+    q, qp = _calls.output(q, "q", (rows, fp8_cols(cols)), torch.uint8, index)
+    scale, sp = _calls.output(scale, "scale", (rows, fp8_scale_pitch(cols)), torch.uint8, index)
+    _check(_lib.sqllm_fp8_quantize(x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else cols, qp, sp, handle),
+           "sqllm_fp8_quantize")
     return q, scale
 
 
+@_calls.on_stream
 def fp8_gemm(q: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: torch.Tensor | None = None,
-             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+             ws: torch.Tensor | None = None, *, index, handle) -> torch.Tensor:
     """y [batch, rows] = x W^T for fp16 x [batch, cols] (or [cols]) and W stored as fp8_quantize leaves it.
     ws: scratch of fp8_workspace_bytes(rows, cols, batch) bytes (a cached one if None)."""
-    dev = _calls.one_device((("q", q), ("scale", scale), ("x", x), ("y", y), ("workspace", ws)))
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x: torch.Tensor expected")
     if x.dim() == 1:
         x = x.unsqueeze(0)
     if x.dim() != 2 or q.dim() != 2:
         raise ValueError(f"x: shape (batch, cols), q: shape (rows, columns) expected, got {tuple(x.shape)}, "
                          f"{tuple(q.shape)}")
     batch, cols = x.shape
-    rows = q.shape[0]
-    if q.shape[1] != fp8_cols(cols) or tuple(scale.shape) != (rows, fp8_scale_pitch(cols)):
+    rows, kept = q.shape
+    if kept != fp8_cols(cols) or tuple(scale.shape) != (rows, fp8_scale_pitch(cols)):
         raise ValueError(f"q, scale: shapes {(rows, fp8_cols(cols))} and {(rows, fp8_scale_pitch(cols))} expected for "
                          f"{cols} columns, got {tuple(q.shape)} and {tuple(scale.shape)}")
-    qp, sp, xp = _dev(q, "q", torch.uint8), _dev(scale, "scale", torch.uint8), _dev(x, "x", torch.float16)
-    with _calls.on(dev, stream):
-        if y is None:
-            y = torch.empty((batch, rows), dtype=torch.float16, device=dev)
-        if tuple(y.shape) != (batch, rows):
-            raise ValueError(f"y: shape {(batch, rows)} expected, got {tuple(y.shape)}")
-        yp, handle = _dev(y, "y", torch.float16), torch.cuda.current_stream().cuda_stream
-        need = fp8_workspace_bytes(rows, cols, batch)
-        with _calls.LOCK:
-            buf = _calls.scratch(need, dev, handle) if ws is None else ws
-            _check(_lib.sqllm_fp8_gemm(qp, sp, rows, cols, xp, batch, yp, _dev(buf, "workspace", torch.uint8),
-                                       buf.numel(), handle), "sqllm_fp8_gemm")
+    qp, sp = _calls.address(q, "q", torch.uint8, index), _calls.address(scale, "scale", torch.uint8, index)
+    xp = _calls.address(x, "x", torch.float16, index)
+    y, yp = _calls.output(y, "y", (batch, rows), torch.float16, index)
+    _check(_calls.with_scratch(ws, fp8_workspace_bytes(rows, cols, batch), index, handle, lambda p, n: _lib.sqllm_fp8_gemm(
+        qp, sp, rows, cols, xp, batch, yp, p, n, handle)), "sqllm_fp8_gemm")
     return y

@@ -3,6 +3,10 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <type_traits>
+
+#include "sqllm_device.h"
 #include "sqllm_fp8.h"
 
 namespace {
@@ -10,10 +14,10 @@ namespace {
 constexpr int kBlock = 128;
 constexpr int64_t kMaxCols = (int64_t)1 << 24;
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+using sqllm::dev::f32x4;
+using sqllm::dev::u32x2;
+using sqllm::dev::u32x4;
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 // ---------------------------------------------------------------------------
 // Quantiser.  Sixteen lanes hold a block, eight values each.  The exponent
@@ -85,32 +89,144 @@ __global__ void __launch_bounds__(256) quantize_kernel(const uint16_t *__restric
 // holds the sum of W row 4 (l / 16) + i and x row l % 16.
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ i32x8 load_piece(const uint8_t *row, int quarter)
+// One product: W rows against x rows, both in the stored form.
+struct Operands {
+    const uint8_t *wq, *wscale, *xq, *xscale;
+    uint16_t *y;
+    int rows, batch, blocks, pitch;
+};
+
+// Four W rows r..r+3 of one x row, rounded once; in one store where the row of
+// y is aligned for it.
+__device__ __forceinline__ void store4(const Operands &p, int b, int r, f32x4 v)
 {
-    const u32x4 lo = *(const u32x4 *)(row + quarter * 16), hi = *(const u32x4 *)(row + 64 + quarter * 16);
-    return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    if (b >= p.batch || r >= p.rows) return;
+    uint16_t *y = p.y + (int64_t)b * p.rows + r;
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __builtin_bit_cast(uint16_t, (_Float16)v[i]);
+    if (r + 4 <= p.rows && ((uintptr_t)y & 7) == 0) {
+        *(u32x2 *)y = u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r + i < p.rows) y[i] = h[i];
 }
 
-__global__ void __launch_bounds__(64) gemm_simple(const uint8_t *__restrict__ wq, const uint8_t *__restrict__ wscale,
-                                                  int rows, const uint8_t *__restrict__ xq,
-                                                  const uint8_t *__restrict__ xscale, int batch, int blocks, int pitch,
-                                                  uint16_t *__restrict__ y)
+__device__ __forceinline__ void lds_load16(const uint8_t *src, uint8_t *lds_base)
 {
-    const int lane = threadIdx.x, n = lane & 15, quarter = lane >> 4;
-    const int r0 = blockIdx.x * 16, b0 = blockIdx.y * 16;
-    const int wr = min(r0 + n, rows - 1), xr = min(b0 + n, batch - 1); // rows past the end: copies, not stored
-    const uint8_t *wp = wq + (int64_t)wr * blocks * kBlock, *xp = xq + (int64_t)xr * blocks * kBlock;
-    const uint8_t *ws = wscale + (int64_t)wr * pitch, *xs = xscale + (int64_t)xr * pitch;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < blocks; ++k)
-        acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(load_piece(wp + k * kBlock, quarter),
-                                                              load_piece(xp + k * kBlock, quarter), acc, 0, 0, 0,
-                                                              (int)ws[k], 0, (int)xs[k]);
-    const int b = b0 + n;
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)src,
+                                     (__attribute__((address_space(3))) uint32_t *)lds_base, 16, 0, 0);
+}
+
+// Tiled form.  A workgroup computes TM rows of W by TN rows of x, each wave WM
+// by WN of them in 16x16 accumulators.  Both operands go through LDS, 128
+// columns (one block) at a time, two stages in turn: the loads of the next
+// stage go straight from memory into LDS while the matrix cores work on this
+// one, and one barrier per stage separates them.  A row's eight 16-byte
+// pieces are stored at piece ^ (row % 8), so that the sixteen rows that a
+// fragment read takes at one piece lie in different banks; the loads into LDS
+// write lane after lane, so the swizzle is in the address they read from.
+template <int TM, int TN, int WM, int WN>
+__global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Operands p)
+{
+    constexpr int W = (TM / WM) * (TN / WN), STAGE = (TM + TN) * kBlock, LOADS = (TM + TN) / 8 / W;
+    static_assert((TM + TN) / 8 % W == 0 && TM / 8 % LOADS == 0, "a wave loads rows of one operand");
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, quarter = lane >> 4;
+    const int mt = (p.rows + TM - 1) / TM, nt = (p.batch + TN - 1) / TN, tiles = mt * nt;
+    // Workgroups go round the eight XCDs: give each a run of tiles, four W
+    // tiles wide, so that the 32 it works on at once share their rows in its L2.
+    constexpr int G = 4;
+    const int per = (tiles + 7) / 8, id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= tiles) return;
+    const int group = id / (G * nt), in = id - group * (G * nt), width = min(G, mt - group * G);
+    const int r0 = (group * G + in % width) * TM, b0 = (in / width) * TN;
+
+    // this wave's loads: 8 rows each of one operand; lane l reads piece
+    // (l % 8) ^ (l / 8) of row l / 8.  Offsets from the tile's first row fit
+    // 32 bits (255 rows of at most 2^24 columns).
+    const uint32_t ld = (uint32_t)p.blocks * kBlock;
+    const bool of_w = w * LOADS * 8 < TM;
+    const uint8_t *src = of_w ? p.wq + (int64_t)r0 * ld : p.xq + (int64_t)b0 * ld;
+    const int most = of_w ? p.rows - 1 - r0 : p.batch - 1 - b0; // rows past the end: copies of the last
+    uint32_t from[LOADS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = r0 + 4 * quarter + i;
-        if (b < batch && r < rows) y[(int64_t)b * rows + r] = __builtin_bit_cast(uint16_t, (_Float16)acc[i]);
+    for (int i = 0; i < LOADS; ++i) {
+        const int row = (w * LOADS + i) * 8 + (lane >> 3) - (of_w ? 0 : TM);
+        from[i] = (uint32_t)min(row, most) * ld + ((lane & 7) ^ (lane >> 3)) * 16;
+    }
+    auto load_stage = [&](int k, int half) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i)
+            lds_load16(src + (uint32_t)k * kBlock + from[i], lds + half * STAGE + (w * LOADS + i) * 1024);
+    };
+
+    constexpr int FM = WM / 16, FN = WN / 16;
+    const int wm = (w % (TM / WM)) * WM, wn = (w / (TM / WM)) * WN;
+    uint32_t ws[FM], xs[FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i) ws[i] = (uint32_t)min(r0 + wm + 16 * i + n, p.rows - 1) * p.pitch;
+#pragma unroll
+    for (int i = 0; i < FN; ++i) xs[i] = (uint32_t)min(b0 + wn + 16 * i + n, p.batch - 1) * p.pitch;
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // byte addresses of this lane's two pieces of fragment row 0, per stage
+    const int piece = n * kBlock + ((quarter ^ (n & 7)) * 16);
+    const uint8_t *a_lo[2], *a_hi[2], *b_lo[2], *b_hi[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        a_lo[h] = lds + h * STAGE + wm * kBlock + piece;
+        a_hi[h] = lds + h * STAGE + wm * kBlock + (piece ^ 64);
+        b_lo[h] = lds + h * STAGE + (TM + wn) * kBlock + piece;
+        b_hi[h] = lds + h * STAGE + (TM + wn) * kBlock + (piece ^ 64);
+    }
+    auto fragment = [&](const uint8_t *plo, const uint8_t *phi) {
+        const u32x4 lo = *(const u32x4 *)plo, hi = *(const u32x4 *)phi;
+        return i32x8{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+
+    int sw[FM], sx[FN]; // scales of four blocks
+    auto stage = [&](int k, auto byte) {
+        constexpr int B = decltype(byte)::value, H = B & 1;
+        __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0): this wave's part of stage k is in LDS
+        __syncthreads();
+        if (k + 1 < p.blocks) load_stage(k + 1, H ^ 1);
+        i32x8 b[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) b[j] = fragment(b_lo[H] + j * 16 * kBlock, b_hi[H] + j * 16 * kBlock);
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const i32x8 a = fragment(a_lo[H] + i * 16 * kBlock, a_hi[H] + i * 16 * kBlock);
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b[j], acc[i][j], 0, 0, B, sw[i], B, sx[j]);
+        }
+    };
+    load_stage(0, 0);
+    for (int k = 0; k < p.blocks; k += 4) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) sw[i] = *(const int *)(p.wscale + ws[i] + k);
+#pragma unroll
+        for (int i = 0; i < FN; ++i) sx[i] = *(const int *)(p.xscale + xs[i] + k);
+        stage(k, std::integral_constant<int, 0>{});
+        if (k + 1 < p.blocks) stage(k + 1, std::integral_constant<int, 1>{});
+        if (k + 2 < p.blocks) stage(k + 2, std::integral_constant<int, 2>{});
+        if (k + 3 < p.blocks) stage(k + 3, std::integral_constant<int, 3>{});
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int b = b0 + wn + 16 * j + n;
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int r = r0 + wm + 16 * i + 4 * quarter;
+            store4(p, b, r, acc[i][j]);
+        }
     }
 }
 
@@ -136,6 +252,17 @@ sqllm_status quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx
     hipLaunchKernelGGL(quantize_kernel, dim3((unsigned)(wgs < 65536 ? wgs : 65536)), dim3(256), 0, stream, x,
                        (uint32_t)(rows * pitch), (int)cols, ldx, blocks, (uint32_t)pitch, q, scale);
     return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
+}
+
+template <int TM, int TN, int WM, int WN>
+void launch_tiled(const Operands &p, hipStream_t stream)
+{
+    auto kern = gemm_tiled<TM, TN, WM, WN>;
+    const size_t lds = 2 * (TM + TN) * kBlock;
+    static std::atomic<uint64_t> asked{0};
+    sqllm::dev::raise_lds_limit((const void *)kern, asked, (int)lds);
+    const int64_t tiles = (int64_t)((p.rows + TM - 1) / TM) * ((p.batch + TN - 1) / TN);
+    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(64 * (TM / WM) * (TN / WN)), lds, stream, p);
 }
 
 } // namespace
@@ -178,8 +305,11 @@ extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, i
     uint8_t *xq = (uint8_t *)workspace, *xs = xq + up256((size_t)batch * sqllm_fp8_cols(cols));
     sqllm_status st = quantize(x, batch, cols, cols, xq, xs, stream);
     if (st != SQLLM_OK) return st;
-    hipLaunchKernelGGL(gemm_simple, dim3((unsigned)((rows + 15) / 16), (unsigned)((batch + 15) / 16)), dim3(64), 0,
-                       stream, q, scale, (int)rows, xq, xs, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
-                       (int)sqllm_fp8_scale_pitch(cols), y);
+    const Operands p = {q, scale, xq, xs, y, (int)rows, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
+                        (int)sqllm_fp8_scale_pitch(cols)};
+    if (rows >= 512 && batch >= 512)
+        launch_tiled<256, 256, 128, 64>(p, stream);
+    else
+        launch_tiled<128, 128, 64, 64>(p, stream);
     return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
 }

@@ -164,6 +164,15 @@ __device__ __forceinline__ void store4(const Operands &p, int b, int r, f32x4 v)
         if (r + i < p.rows) y[i] = h[i];
 }
 
+// The same of split blockIdx.y, unrounded.
+__device__ __forceinline__ void store_partial(const Operands &p, float *partial, int b, int r, f32x4 v)
+{
+    if (b >= p.batch) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r + i < p.rows) partial[((int64_t)blockIdx.y * p.batch + b) * p.rows + r + i] = v[i];
+}
+
 // Each lane's 16 (4) bytes at src to lds_base + 16 (4) * lane.
 __device__ __forceinline__ void lds_load16(const uint8_t *src, uint8_t *lds_base)
 {
@@ -319,10 +328,8 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
             const int r = r0 + wm + 16 * i + 4 * quarter;
             if (splits == 1)
                 store4(p, b, r, acc[i][j]);
-            else if (b < p.batch)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (r + q < p.rows) partial[((int64_t)blockIdx.y * p.batch + b) * p.rows + r + q] = acc[i][j][q];
+            else
+                store_partial(p, partial, b, r, acc[i][j]);
         }
     }
 }
@@ -463,13 +470,18 @@ __global__ void __launch_bounds__(256) add_splits(const float *partial, int64_t 
     }
 }
 
-// Streaming form, for batches of at most 16: W is read once, straight into
-// the registers of one 16x16 step, and everything else hides behind that.  A
-// wave takes 16 R rows of W and every waves-th block of columns, with D steps
-// of loads in flight; the waves' sums are added in LDS.  FUSED: x comes in
-// fp16 and each wave rounds the block it needs (about 60 vector instructions
-// against the 2 R KB of W that the step reads); else in the stored form, for
-// rows of x that cannot be read 16 bytes at a time.
+// Streaming form, for batches of at most 16: W is read once and everything
+// else hides behind that.  A wave takes 16 R rows of W and every waves-th
+// block of columns, D steps of loads in flight; the waves' sums are added in
+// LDS.  W goes straight into LDS, each wave to a ring of its own (no barrier):
+// an instruction reads whole 128-byte lines of eight rows, where loads into
+// the matrix cores' register layout read 64 bytes of sixteen, which the memory
+// answers a quarter slower (8192x8192: 19 us against 15).  FUSED: x comes in
+// fp16 and each wave rounds the block it needs, about 80 vector instructions
+// against the 2 R KB of W that the step reads; else in the stored form.  Few
+// rows: the columns are split over `splits` workgroups, their sums going to
+// partial[split][batch][rows].
+
 // Keeps a uniform address in scalar registers, so that the loads add a 32-bit
 // lane offset to it (otherwise each load gets a running 64-bit address of its
 // own in vector registers).
@@ -488,47 +500,64 @@ __device__ __forceinline__ T load_at(global_ptr base, uint32_t offset)
     return *(const __attribute__((address_space(1))) T *)(base + offset);
 }
 
+constexpr int kStreamWaves = 8;
+
+template <int R>
+constexpr int stream_depth() { return R == 1 ? 4 : 3; }
+
+template <int R>
+constexpr size_t stream_lds() { return (size_t)kStreamWaves * stream_depth<R>() * R * 2048; }
+
 template <int R, bool FUSED>
 struct StreamStep {
-    u32x4 w[R][2];
     uint32_t ws[R];
     u32x4 x[FUSED ? 4 : 2];
     uint32_t xs;
 };
 
 template <int R, bool FUSED>
-__global__ void __launch_bounds__(1024, 4) gemm_stream(Operands p, const uint16_t *x, int cols)
+__global__ void __launch_bounds__(64 * kStreamWaves, 4) gemm_stream(Operands p, const uint16_t *x, int cols, int splits, float *partial)
 {
-    constexpr int D = R == 2 && FUSED ? 2 : 3; // as many as fit 128 registers
-    __shared__ __align__(16) float red[16][R][64][4];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    constexpr int D = stream_depth<R>(), kLoads = 3 * R + (FUSED ? 4 : 3); // loads of a step
+    extern __shared__ __align__(16) uint8_t lds[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, quarter = lane >> 4, r0 = blockIdx.x * 16 * R;
+    uint8_t *const own = lds + w * D * R * 2048;
     // lane offsets from the tile's first row and from x fit 32 bits (at most 32
-    // rows of 2^24 columns)
+    // rows of 2^24 columns); rows past the last are copies, not stored
     const uint32_t ld = (uint32_t)p.blocks * kBlock;
     const uint8_t *wbase = p.wq + (int64_t)r0 * ld, *wsbase = p.wscale + (int64_t)r0 * p.pitch;
-    uint32_t wp[R], wsp[R];
+    uint32_t from[2 * R], wsp[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) { // rows past the last: copies, not stored
-        const uint32_t row = min(16 * i + n, p.rows - 1 - r0);
-        wp[i] = row * ld + quarter * 16;
-        wsp[i] = row * p.pitch;
-    }
+    for (int i = 0; i < 2 * R; ++i)
+        from[i] = (uint32_t)min(8 * i + (lane >> 3), p.rows - 1 - r0) * ld + ((lane & 7) ^ (lane >> 3)) * 16;
+#pragma unroll
+    for (int i = 0; i < R; ++i) wsp[i] = (uint32_t)min(16 * i + n, p.rows - 1 - r0) * p.pitch;
     const uint32_t xr = min(n, p.batch - 1), xf = xr * (uint32_t)cols, xq = xr * ld + quarter * 16, xs = xr * p.pitch;
-    const int steps = max(0, (p.blocks - w + waves - 1) / waves);
+    const int worker = blockIdx.y * kStreamWaves + w, workers = splits * kStreamWaves;
+    const int steps = max(0, (p.blocks - worker + workers - 1) / workers);
+    // A wave's i-th block.  Workgroups start at different ones: where the rows
+    // are a power of two apart, the same block of all rows would lie in a few
+    // of the memory's channels.
+    const int turn = (int)(blockIdx.x * (uint32_t)kStreamWaves % (uint32_t)p.blocks);
+    auto block_of = [&](int i) {
+        const int k = worker + i * workers + turn;
+        return k >= p.blocks ? k - p.blocks : k;
+    };
     // first column of piece h of block k that this lane quantises
     auto column = [&](int k, int h) { return k * kBlock + (h >> 1) * 64 + (h & 1) * 8 + quarter * 16; };
     StreamStep<R, FUSED> ring[D];
-    // every step issues the same loads; past the wave's last block they read that again
-    auto load = [&](StreamStep<R, FUSED> &s, int i) {
-        const int k = max(0, min(w + i * waves, w + (steps - 1) * waves));
-        const global_ptr wk = scalar(wbase + (uint32_t)k * kBlock), wsk = scalar(wsbase + k);
+    // every step issues the same loads in the same order, so that their count
+    // tells which have arrived; past the wave's last block they read one again
+    auto load = [&](int slot, int i) {
+        StreamStep<R, FUSED> &s = ring[slot];
+        const int k = steps ? block_of(min(i, steps - 1)) : 0;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            s.w[r][0] = load_at<u32x4>(wk, wp[r]);
-            s.w[r][1] = load_at<u32x4>(wk, wp[r] + 64);
-            s.ws[r] = load_at<uint8_t>(wsk, wsp[r]);
-        }
+        for (int j = 0; j < 2 * R; ++j)
+            lds_load16(wbase + (uint32_t)k * kBlock + from[j], own + slot * R * 2048 + j * 1024);
+        const global_ptr wsk = scalar(wsbase + k);
+#pragma unroll
+        for (int r = 0; r < R; ++r) s.ws[r] = load_at<uint8_t>(wsk, wsp[r]);
         if constexpr (FUSED) {
             // past the row's end (cols is a multiple of 8) its last eight, zeroed at use
 #pragma unroll
@@ -539,17 +568,21 @@ __global__ void __launch_bounds__(1024, 4) gemm_stream(Operands p, const uint16_
             s.x[1] = load_at<u32x4>(xk, xq + 64);
             s.xs = load_at<uint8_t>(xsk, xs);
         }
-        asm volatile("" ::: "memory"); // loads stay in this order: the waits count them
+        asm volatile("" ::: "memory"); // loads stay in this order
         __builtin_amdgcn_sched_barrier(0);
     };
+    const int piece = n * kBlock + ((quarter ^ (n & 7)) * 16);
     f32x4 acc[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) acc[r] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto multiply = [&](const StreamStep<R, FUSED> &s, int i) {
+    auto multiply = [&](int slot, int i) {
+        const StreamStep<R, FUSED> &s = ring[slot];
+        wait_loads<(D - 1) * kLoads>(); // this step's are there
+        asm volatile("" ::: "memory");
         i32x8 b;
         uint32_t sb;
         if constexpr (FUSED) {
-            const int k = w + i * waves;
+            const int k = block_of(i);
             uint32_t v[16];
 #pragma unroll
             for (int h = 0; h < 4; ++h) {
@@ -571,31 +604,40 @@ __global__ void __launch_bounds__(1024, 4) gemm_stream(Operands p, const uint16_
         }
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            const i32x8 a = {(int)s.w[r][0].x, (int)s.w[r][0].y, (int)s.w[r][0].z, (int)s.w[r][0].w,
-                             (int)s.w[r][1].x, (int)s.w[r][1].y, (int)s.w[r][1].z, (int)s.w[r][1].w};
+            const uint8_t *at = own + (slot * R + r) * 2048;
+            const u32x4 lo = *(const u32x4 *)(at + piece), hi = *(const u32x4 *)(at + (piece ^ 64));
+            const i32x8 a = {(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
             acc[r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc[r], 0, 0, 0, (int)s.ws[r], 0, (int)sb);
         }
+        __builtin_amdgcn_sched_barrier(0); // the reads of this slot before the loads into it
     };
 #pragma unroll
-    for (int k = 0; k < D; ++k) load(ring[k], k);
+    for (int k = 0; k < D; ++k) load(k, k);
     int i = 0;
     for (; i + D <= steps; i += D) {
 #pragma unroll
         for (int k = 0; k < D; ++k) {
-            multiply(ring[k], i + k);
-            load(ring[k], i + k + D);
+            multiply(k, i + k);
+            load(k, i + k + D);
         }
     }
+    // the last steps issue no loads: fewer are in flight than multiply counts on
+    wait_loads<0>();
 #pragma unroll
     for (int k = 0; k < D - 1; ++k)
-        if (i + k < steps) multiply(ring[k], i + k);
+        if (i + k < steps) multiply(k, i + k);
+    __syncthreads(); // the rings are done with: their LDS takes the sums
+    f32x4 *const red = (f32x4 *)lds;
 #pragma unroll
-    for (int r = 0; r < R; ++r) *(f32x4 *)red[w][r][lane] = acc[r];
+    for (int r = 0; r < R; ++r) red[(w * R + r) * 64 + lane] = acc[r];
     __syncthreads();
-    for (int r = w; r < R; r += waves) {
+    for (int r = w; r < R; r += kStreamWaves) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
-        for (int k = 0; k < waves; ++k) v += *(const f32x4 *)red[k][r][lane];
-        store4(p, n, r0 + 16 * r + 4 * quarter, v);
+        for (int k = 0; k < kStreamWaves; ++k) v += red[(k * R + r) * 64 + lane];
+        if (splits == 1)
+            store4(p, n, r0 + 16 * r + 4 * quarter, v);
+        else
+            store_partial(p, partial, n, r0 + 16 * r + 4 * quarter, v);
     }
 }
 
@@ -624,20 +666,32 @@ sqllm_status quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx
     return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
 }
 
-// Two groups of 16 rows a wave from 8192 rows on, where that still gives
-// every compute unit a workgroup: half the activations are read and rounded
-// (8192x22016: 48 us against 49 at batch 1, 62 against 80 at batch 16;
-// 4096x4096: 11.6 against 8.6).
-// Below one workgroup a unit, sixteen waves instead of eight share a tile's
-// columns.
-template <bool FUSED>
-void launch_stream(const Operands &p, const uint16_t *x, int cols, hipStream_t stream)
+void launch_add(const Operands &p, int splits, const float *partial, hipStream_t stream)
 {
-    if (p.rows >= 8192)
-        hipLaunchKernelGGL((gemm_stream<2, FUSED>), dim3((p.rows + 31) / 32), dim3(512), 0, stream, p, x, cols);
-    else
-        hipLaunchKernelGGL((gemm_stream<1, FUSED>), dim3((p.rows + 15) / 16), dim3(512), 0, stream,
-                           p, x, cols);
+    const int64_t total = (int64_t)p.batch * p.rows, wgs = (total + 255) / 256;
+    hipLaunchKernelGGL(add_splits, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, stream, partial, total, splits,
+                       p.y);
+}
+
+// Splits of a streamed product's columns: while few rows give half of the
+// compute units no workgroup and every wave keeps at least eight blocks.
+int stream_splits(int64_t rows, int64_t blocks)
+{
+    int s = 1;
+    while (s < 8 && rows * s <= 16 * 128 && blocks >= 2 * s * 8 * kStreamWaves) s *= 2;
+    return s;
+}
+
+template <int R, bool FUSED>
+void launch_stream(const Operands &p, const uint16_t *x, int cols, float *partial, hipStream_t stream)
+{
+    auto kern = gemm_stream<R, FUSED>;
+    static std::atomic<uint64_t> asked{0};
+    sqllm::dev::raise_lds_limit((const void *)kern, asked, (int)stream_lds<R>());
+    const int splits = stream_splits(p.rows, p.blocks);
+    hipLaunchKernelGGL(kern, dim3((p.rows + 16 * R - 1) / (16 * R), splits), dim3(64 * kStreamWaves), stream_lds<R>(),
+                       stream, p, x, cols, splits, partial);
+    if (splits > 1) launch_add(p, splits, partial, stream);
 }
 
 template <int TM, int TN, int WM, int WN, int S>
@@ -650,11 +704,7 @@ void launch_tiled(const Operands &p, int splits, float *partial, hipStream_t str
     const int64_t tiles = (int64_t)((p.rows + TM - 1) / TM) * ((p.batch + TN - 1) / TN);
     hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(64 * T::W), T::kLds, stream, p, splits,
                        partial);
-    if (splits > 1) {
-        const int64_t total = (int64_t)p.batch * p.rows, wgs = (total + 255) / 256;
-        hipLaunchKernelGGL(add_splits, dim3((unsigned)(wgs < 4096 ? wgs : 4096)), dim3(256), 0, stream, partial, total,
-                           splits, p.y);
-    }
+    if (splits > 1) launch_add(p, splits, partial, stream);
 }
 
 void launch_large(const Operands &p, hipStream_t stream)
@@ -728,7 +778,7 @@ extern "C" sqllm_status sqllm_fp8_quantize(const uint16_t *x, int64_t rows, int6
 extern "C" size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
 {
     if (!good_shape(rows, cols) || batch < 1 || !good_shape(batch, cols)) return 0;
-    const int splits = batch <= 16 ? 1 : choose(rows, cols, batch).splits;
+    const int splits = batch <= 16 ? stream_splits(rows, sqllm_fp8_cols(cols) / kBlock) : choose(rows, cols, batch).splits;
     return up256((size_t)batch * sqllm_fp8_cols(cols)) + up256((size_t)batch * sqllm_fp8_scale_pitch(cols)) +
            (splits > 1 ? (size_t)splits * batch * rows * 4 : 0);
 }
@@ -746,16 +796,24 @@ extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, i
     uint8_t *xq = (uint8_t *)workspace, *xs = xq + up256((size_t)batch * sqllm_fp8_cols(cols));
     const Operands p = {q, scale, xq, xs, y, (int)rows, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
                         (int)sqllm_fp8_scale_pitch(cols)};
-    if (batch <= 16 && aligned(x, 16) && cols % 8 == 0) {
-        launch_stream<true>(p, x, (int)cols, stream);
+    float *partial = (float *)(xs + up256((size_t)batch * sqllm_fp8_scale_pitch(cols)));
+    // A small matrix for a few rows of x: one launch that rounds x as it goes
+    // (4096x4096 at batch 1: 8.3 us against 2.2 and 6.5 in two launches, at
+    // batch 16 13.6 against 3.3 and 10.8).
+    if (batch <= 8 && rows * cols <= 1 << 24 && aligned(x, 16) && cols % 8 == 0) {
+        launch_stream<1, true>(p, x, (int)cols, partial, stream);
         return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
     }
     const sqllm_status st = quantize(x, batch, cols, cols, xq, xs, stream);
     if (st != SQLLM_OK) return st;
-    if (batch <= 16)
-        launch_stream<false>(p, x, (int)cols, stream);
+    // Two groups of 16 rows a wave halve the reads of x, where there are rows
+    // enough (8192x22016: 33 us either way at batch 1, 39 against 46 at batch
+    // 16; 4096x4096: 7.7 against 6.5).
+    if (batch <= 16 && rows >= 8192)
+        launch_stream<2, false>(p, x, (int)cols, partial, stream);
+    else if (batch <= 16)
+        launch_stream<1, false>(p, x, (int)cols, partial, stream);
     else
-        launch_choice(choose(rows, cols, batch), p, (float *)(xs + up256((size_t)batch * sqllm_fp8_scale_pitch(cols))),
-                      stream);
+        launch_choice(choose(rows, cols, batch), p, partial, stream);
     return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
 }

@@ -157,6 +157,7 @@ SHAPES = [(1, 1, 1), (1, 16, 128), (1, 300, 4096), (2, 129, 127), (3, 64, 8320),
           (17, 64, 256), (17, 300, 130), (31, 1000, 1300), (33, 130, 512), (64, 256, 4096), (65, 127, 700),
           (128, 128, 128), (129, 513, 1024), (200, 70, 3000), (255, 256, 640), (257, 255, 1152), (512, 768, 2000),
           (1000, 300, 300), (1, 5000, 22016), (40, 2304, 6400), (300, 2560, 1536),
+          (1, 130, 20008), (11, 300, 24000), (16, 2000, 16500), (16, 8200, 512), (5, 8193, 300),
           (3600, 3590, 130), (3400, 3841, 640), (3585, 3500, 1000)]
 
 

@@ -8,6 +8,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <atomic>
 #include <utility>
 
 #include "sqllm_device.h"
@@ -59,12 +61,30 @@ __device__ __forceinline__ void row_sums(const uint16_t *const (&w)[R], const ui
     }
 }
 
-// The sum over the wave's lanes, in every lane.
+// v of lane l - N of the same row of 16, or of the last lane of the rows before
+// (DPP row_shr, row_bcast); 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_double(double v)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, true);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+
+// The sum over the wave's lanes, in every lane: a prefix sum by DPP shifts
+// within rows of 16 and broadcasts across them, of which lane 63 has the last.
 __device__ __forceinline__ double wave_sum(double v)
 {
-#pragma unroll
-    for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+    v += dpp_double<0x111, 0xF>(v); // row_shr 1, 2, 4, 8
+    v += dpp_double<0x112, 0xF>(v);
+    v += dpp_double<0x114, 0xF>(v);
+    v += dpp_double<0x118, 0xF>(v);
+    v += dpp_double<0x142, 0xA>(v); // row_bcast 15, 31
+    v += dpp_double<0x143, 0xC>(v);
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)b, 63), hi = __builtin_amdgcn_readlane((uint32_t)(b >> 32), 63);
+    return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
 }
 
 // A double's place in ascending order as an unsigned number; NaN is 0, below
@@ -108,11 +128,13 @@ __device__ __forceinline__ void choose(L logit, const float *bias, int experts, 
 #pragma unroll
         for (int j = 0; j < N; ++j) s[j] = 1.0 / (1.0 + exp(-s[j]));
     } else {
-        double top = s[0], sum = 0.0;
+        // exp(s - top) for any top near the largest: its upper half will do
+        uint32_t most = 0;
 #pragma unroll
-        for (int j = 1; j < N; ++j) top = fmax(top, s[j]);
-#pragma unroll
-        for (int m = 32; m; m >>= 1) top = fmax(top, __shfl_xor(top, m));
+        for (int j = 0; j < N; ++j) most = max(most, (uint32_t)(order_key(s[j]) >> 32));
+        most = wave_max(most);
+        const double top = __longlong_as_double((long long)((uint64_t)(most >> 31 ? most ^ 0x80000000u : ~most) << 32));
+        double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             s[j] = lane + 64 * j < experts ? exp(s[j] - top) : 0.0;
@@ -424,12 +446,12 @@ __device__ __forceinline__ Chosen find_chosen(const int32_t *ids, int pairs, int
     if (e1 >= 0) atomicOr(&lds.bitmap[e1 >> 5], 1u << (e1 & 31));
     wave_sync();
     const uint32_t word = lane < kMaxExperts / 32 ? lds.bitmap[lane] : 0;
-    int before = __popc(word); // running count over the sixteen words
-#pragma unroll
-    for (int m = 1; m < kMaxExperts / 32; m <<= 1) {
-        const int o = __shfl_up(before, m);
-        if (lane >= m) before += o;
-    }
+    int before = __popc(word); // running count over the sixteen words, in one row of lanes
+    static_assert(kMaxExperts / 32 == 16, "one row of lanes");
+    before += __builtin_amdgcn_update_dpp(0, before, 0x111, 0xF, 0xF, true); // row_shr 1, 2, 4, 8
+    before += __builtin_amdgcn_update_dpp(0, before, 0x112, 0xF, 0xF, true);
+    before += __builtin_amdgcn_update_dpp(0, before, 0x114, 0xF, 0xF, true);
+    before += __builtin_amdgcn_update_dpp(0, before, 0x118, 0xF, 0xF, true);
     const uint64_t past = __ballot(lane < kMaxExperts / 32 && before > slot);
     if (past == 0) return {-1, 0};
     const int at = __builtin_ctzll(past);
@@ -467,15 +489,113 @@ __device__ __forceinline__ void add_chunk(uint32_t val, float x, int cb, int v1,
     if (present) sum += first > 0 ? top - below : top;
 }
 
+// A wave's share of a tile's outliers, in one of two forms.
+//   By rows: lane = row takes entries 4 share .. 4 share + 3 of its row, then
+//     those 4 `shares` further, four at a load.  About 30 vector instructions
+//     a step and 8 a token.
+//   By chunks: an even part [v0, v1) of the tile's nonzeros, 64 at a time, a
+//     nonzero per lane (add_chunk): about 65 instructions a chunk and token,
+//     whatever the rows hold.
+// By rows unless the fullest row would take more than twice as many steps as
+// there are chunks (16 tokens, 128 experts 1536x4096 at 0.45%: gate and up 87
+// us by rows, 90 by chunks, 72 without outliers; 8 experts 3584x4096, 4 bits:
+// 40, 44 and 37).
+struct Outliers {
+    const uint16_t *cols, *vals; // the tile's
+    int lo, count;               // this lane's row: entries [lo, lo + count)
+    int len;                     // the tile's
+    int share, shares;
+    int64_t left;                // entries from the tile's first to the arrays' end
+
+    __device__ __forceinline__ void set(const Projection &p, int rp_lo, int rp_hi, int worker, int workers)
+    {
+        const int nz0 = __builtin_amdgcn_readfirstlane(rp_lo); // all else relative to the tile's first
+        lo = rp_lo - nz0, count = rp_hi - rp_lo;
+        len = __builtin_amdgcn_readlane(rp_hi, 63) - nz0;
+        cols = p.col + nz0, vals = p.val + nz0;
+        share = worker, shares = workers;
+        left = p.nnz - nz0;
+    }
+
+    // Their products with the tokens' activations value(j, c), into sum[j].
+    template <int T, int N, typename V>
+    __device__ __forceinline__ void add(int tokens, V value, float (&sum)[N]) const
+    {
+        const int steps = ((int)wave_max((uint32_t)count) + 4 * shares - 1) / (4 * shares);
+        const int chunks = (len + 64 * shares - 1) / (64 * shares);
+        if (left >= 4 && steps <= 2 * chunks)
+            by_rows<T>(tokens, value, sum, steps);
+        else
+            by_chunks<T>(tokens, value, sum);
+    }
+
+    template <int T, int N, typename V>
+    __device__ __forceinline__ void by_rows(int tokens, V value, float (&sum)[N], int steps) const
+    {
+        for (int n = 0; n < steps; ++n) {
+            const int first = 4 * (share + n * shares); // of the row
+            // four entries at once, from further left at the end of the arrays
+            const int64_t at = min(lo + (int64_t)min(first, max(count - 1, 0)), left - 1), from = min(at, left - 4);
+            const int skip = 16 * (int)(at - from);
+            uint64_t c, v;
+            __builtin_memcpy(&c, cols + from, 8);
+            __builtin_memcpy(&v, vals + from, 8);
+            c >>= skip, v >>= skip;
+            float w[4];
+            int col[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) { // entries past the row's count zero; their columns are some entry's
+                col[k] = (int)(c >> (16 * k)) & 0xFFFF;
+                w[k] = first + k < count ? dev::f16_to_f32((uint16_t)(v >> (16 * k))) : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+                if (j < tokens) {
+                    float xv[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) xv[k] = value(j, col[k]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sum[j] += w[k] * xv[k];
+                }
+        }
+    }
+
+    template <int T, int N, typename V>
+    __device__ __forceinline__ void by_chunks(int tokens, V value, float (&sum)[N]) const
+    {
+        const int lane = threadIdx.x & 63, per = len / shares, extra = len - per * shares;
+        const int v0 = share * per + min(share, extra), v1 = v0 + per + (share < extra ? 1 : 0);
+        constexpr int kAtOnce = 2;
+        for (int base = v0; base < v1; base += 64 * kAtOnce) {
+            int col[kAtOnce];
+            uint32_t val[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) { // past the last: that one again, dropped by add_chunk
+                const int at = min(base + 64 * k + lane, v1 - 1);
+                col[k] = cols[at];
+                val[k] = vals[at];
+            }
+#pragma unroll
+            for (int j = 0; j < T; ++j)
+                if (j < tokens) {
+                    float xv[kAtOnce];
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k) xv[k] = value(j, col[k]);
+#pragma unroll
+                    for (int k = 0; k < kAtOnce; ++k)
+                        if (base + 64 * k < v1)
+                            add_chunk(val[k], xv[k], base + 64 * k, v1, lane, lo, lo + count, sum[j]);
+                }
+        }
+    }
+};
+
 // This wave's share (worker `worker` of `workers`) of one matrix for one tile:
-// every workers-th half group, and a contiguous range of the tile's nonzeros.
-// x(j) is the fp16 row of matrix column j, and value(j, c) the activation of
-// token j at column c in fp32, for the outliers of tokens below `tokens`.
-// Column 4h + i of the matrix steps ends in sum[4h + i]; an outlier of token j
-// is added to sum[j].
-template <int BITS, int NQ, int T, typename X, typename V>
-__device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int groups, int worker, int workers,
-                                             int tokens, X x, V value, float (&sum)[4 * NQ])
+// every workers-th half group; its share of the outliers is left in `out`.  x(j) is the fp16 row of matrix column j.
+// Column 4h + i of the matrix steps ends in sum[4h + i].
+template <int BITS, int NQ, typename X>
+__device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int groups, int worker, int workers, X x,
+                                             float (&sum)[4 * NQ], Outliers &out)
 {
     // half groups in flight, as many as fit 128 registers without spilling
     constexpr int D = NQ == 1 ? (BITS == 2 ? 3 : 4) : (NQ == 2 ? (BITS == 2 ? 2 : 3) : (NQ == 4 && BITS == 3 ? 2 : 1));
@@ -484,8 +604,8 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
     const int64_t row = tile * 64 + lane;
     Table<BITS> table;
     table.load(p.lut + (row << BITS));
-    int rp_lo = 0, rp_hi = 0;
-    if (p.nnz) rp_lo = p.row_ptr[row], rp_hi = p.row_ptr[row + 1];
+    const int32_t *rp = p.nnz ? p.row_ptr + row : (const int32_t *)dev::g_placeholder;
+    const int rp_lo = rp[0], rp_hi = rp[1];
     const int n = max(0, (2 * groups - worker + workers - 1) / workers); // half groups of this wave
     const uint8_t *codes = p.packed + tile * groups * (2 * BITS * 1024);
     const uint16_t *xr[NQ];
@@ -531,6 +651,7 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
     };
 #pragma unroll
     for (int k = 0; k < D; ++k) load(k, k);
+    out.set(p, rp_lo, rp_hi, worker, workers);
     int i = 0;
     for (; i + D <= n; i += D) {
 #pragma unroll
@@ -546,35 +667,29 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
     for (int h = 0; h < NQ; ++h)
 #pragma unroll
         for (int r = 0; r < 4; ++r) sum[4 * h + r] = C == 2 ? acc[h][0][r] + acc[h][C - 1][r] : acc[h][0][r];
-    // outliers: a nonzero per lane, kChunks of 64 at a time so that a round
-    // waits for memory twice; a prefix sum over the wave gives every row's
-    // run of products as a difference
-    if (p.nnz == 0) return;
-    constexpr int kChunks = 4;
-    const int nz0 = __builtin_amdgcn_readfirstlane(rp_lo); // all else relative to the tile's first nonzero
-    rp_lo -= nz0, rp_hi -= nz0;
-    const int len = __builtin_amdgcn_readlane(rp_hi, 63), per = len / workers, extra = len - per * workers;
-    const int v0 = worker * per + min(worker, extra), v1 = v0 + per + (worker < extra ? 1 : 0);
-    const uint16_t *cols = p.col + nz0, *vals = p.val + nz0;
-    for (int base = v0; base < v1; base += 64 * kChunks) {
-        int col[kChunks];
-        uint32_t val[kChunks];
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) { // past the last: that one again, dropped by the scan
-            const int n = min(base + 64 * k + lane, v1 - 1);
-            col[k] = cols[n];
-            val[k] = vals[n];
-        }
-#pragma unroll
-        for (int j = 0; j < T; ++j)
-            if (j < tokens) {
-                float xv[kChunks];
-#pragma unroll
-                for (int k = 0; k < kChunks; ++k) xv[k] = value(j, col[k]);
-#pragma unroll
-                for (int k = 0; k < kChunks; ++k)
-                    if (base + 64 * k < v1) add_chunk(val[k], xv[k], base + 64 * k, v1, lane, rp_lo, rp_hi, sum[j]);
-            }
+}
+
+// Every wave's loads into LDS have arrived.
+__device__ __forceinline__ void all_loads_done()
+{
+    __builtin_amdgcn_s_waitcnt(0x0F70); // vmcnt(0)
+    __syncthreads();
+}
+
+// Copies `rows` rows of `bytes` (a multiple of 512) into LDS, row j from
+// source(j), 1 KB or the rest of a row per instruction, straight from memory;
+// they are there once the caller's later loads are and all waves have met.
+template <typename S>
+__device__ __forceinline__ void stage_rows(int rows, int bytes, S source, uint8_t *lds)
+{
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    for (int j = 0; j < rows; ++j) {
+        const uint8_t *src = source(j);
+        for (int at = w * 1024; at < bytes; at += kDefaultWaves * 1024)
+            if (at + lane * 16 < bytes)
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)(src + at + lane * 16),
+                                                 (__attribute__((address_space(3))) uint32_t *)(lds + j * bytes + at), 16,
+                                                 0, 0);
     }
 }
 
@@ -596,17 +711,30 @@ struct Activations { // [pair][inter]
 template <int BITS, int NQ>
 __device__ __forceinline__ void gate_up_body(const Projection &gate, const Projection &up, const uint16_t *x,
                                              const ChosenLds &lds, Chosen c, int topk, int hidden, int inter,
-                                             Activations a, float *red)
+                                             int room, Activations a, uint8_t *space)
 {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x;
     const int64_t tile = (int64_t)c.expert * (inter >> 6) + t;
     auto row_of = [&](int j) { return x + (int64_t)(lds.list[j] & 255) * hidden; };
+    const int64_t own_nnz = w & 1 ? up.nnz : gate.nnz;
+    const bool staged = c.count * hidden * 2 <= room && gate.nnz + up.nnz > 0;
+    if (staged)
+        stage_rows(c.count, hidden * 2, [&](int j) { return (const uint8_t *)row_of(j); }, space);
     float sum[4 * NQ];
-    tile_product<BITS, NQ, 4 * NQ>(
-        w & 1 ? up : gate, tile, hidden >> 8, w >> 1, kDefaultWaves / 2, c.count,
-        [&](int j) { return row_of(min(j, c.count - 1)); }, // past the last: a copy, whose sums are dropped
-        [&](int j, int col) { return dev::f16_to_f32(row_of(j)[col]); }, sum);
+    Outliers out;
+    tile_product<BITS, NQ>(w & 1 ? up : gate, tile, hidden >> 8, w >> 1, kDefaultWaves / 2,
+                           [&](int j) { return row_of(min(j, c.count - 1)); }, // past the last: a copy, dropped
+                           sum, out);
+    if (staged) {
+        all_loads_done();
+        const uint16_t *xs = (const uint16_t *)space;
+        if (own_nnz) out.add<4 * NQ>(c.count, [&](int j, int col) { return dev::f16_to_f32(xs[j * hidden + col]); }, sum);
+        __syncthreads(); // the space is used again below
+    } else if (own_nnz) {
+        out.add<4 * NQ>(c.count, [&](int j, int col) { return dev::f16_to_f32(row_of(j)[col]); }, sum);
+    }
+    float *const red = (float *)space;
 #pragma unroll
     for (int j = 0; j < 4 * NQ; ++j) red[(w * 4 * NQ + j) * 64 + lane] = sum[j];
     __syncthreads();
@@ -631,19 +759,19 @@ __device__ __forceinline__ void gate_up_body(const Projection &gate, const Proje
 template <int BITS, int MAXQ>
 __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Projection gate, Projection up, const uint16_t *x,
                                                                   const int32_t *ids, int batch, int experts, int topk,
-                                                                  int hidden, int inter, Activations a)
+                                                                  int hidden, int inter, int room, Activations a)
 {
     __shared__ ChosenLds chosen[kDefaultWaves];
-    extern __shared__ float red[];
+    extern __shared__ __align__(16) uint8_t space[];
     ChosenLds &lds = chosen[threadIdx.x >> 6];
     const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
     if (c.expert < 0) return;
     if (MAXQ >= 4 && c.count > 8)
-        gate_up_body<BITS, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, a, red);
+        gate_up_body<BITS, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
     else if (MAXQ >= 2 && c.count > 4)
-        gate_up_body<BITS, MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, a, red);
+        gate_up_body<BITS, MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
     else
-        gate_up_body<BITS, 1>(gate, up, x, lds, c, topk, hidden, inter, a, red);
+        gate_up_body<BITS, 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
 }
 
 // ---------------------------------------------------------------------------
@@ -654,8 +782,8 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Project
 // ---------------------------------------------------------------------------
 template <int BITS, int NQ>
 __device__ __forceinline__ void down_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
-                                          int topk, int hidden, int inter, int parts, int64_t pairs, float *partial,
-                                          float *red)
+                                          int topk, int hidden, int inter, int parts, int room, int64_t pairs,
+                                          float *partial, uint8_t *space)
 {
     constexpr int T = 2 * NQ; // tokens
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -663,18 +791,29 @@ __device__ __forceinline__ void down_body(const Projection &down, Activations a,
     const bool owns = t < tiles; // the last workgroup may have waves too many
     const int64_t tile = (int64_t)c.expert * tiles + min(t, tiles - 1);
     auto pair_of = [&](int j) { return (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8); };
-    float *out = partial + blockIdx.z * pairs * hidden + t * 64 + lane;
+    float *const to = partial + blockIdx.z * pairs * hidden + t * 64 + lane;
     float sum[4 * NQ];
     const int workers = parts * gridDim.z, worker = blockIdx.z * parts + part;
-    if (owns)
-        tile_product<BITS, NQ, T>(
-            down, tile, inter >> 8, worker, workers, c.count,
-            [&](int j) { return (j < T ? a.hi : a.lo) + pair_of(min(j & (T - 1), c.count - 1)) * inter; },
-            [&](int j, int col) { return a.whole[pair_of(j) * inter + col]; }, sum);
+    auto whole_of = [&](int j) { return a.whole + pair_of(j) * inter; };
+    const bool staged = c.count * inter * 4 <= room && down.nnz > 0;
+    if (staged) stage_rows(c.count, inter * 4, [&](int j) { return (const uint8_t *)whole_of(j); }, space);
+    Outliers out;
+    tile_product<BITS, NQ>(down, tile, inter >> 8, worker, workers,
+                           [&](int j) { return (j < T ? a.hi : a.lo) + pair_of(min(j & (T - 1), c.count - 1)) * inter; },
+                           sum, out);
+    if (staged) {
+        all_loads_done();
+        const float *xs = (const float *)space;
+        out.add<T>(c.count, [&](int j, int col) { return xs[j * inter + col]; }, sum);
+        __syncthreads(); // the space is used again below
+    } else if (down.nnz > 0) {
+        out.add<T>(c.count, [&](int j, int col) { return whole_of(j)[col]; }, sum);
+    }
+    float *const red = (float *)space;
     if (parts == 1) {
 #pragma unroll
         for (int j = 0; j < T; ++j)
-            if (owns && j < c.count) out[pair_of(j) * hidden] = sum[j] + sum[T + j];
+            if (owns && j < c.count) to[pair_of(j) * hidden] = sum[j] + sum[T + j];
         return;
     }
 #pragma unroll
@@ -684,7 +823,7 @@ __device__ __forceinline__ void down_body(const Projection &down, Activations a,
     for (int j = part; j < c.count; j += parts) {
         float v = 0.f;
         for (int k = w0; k < w0 + parts; ++k) v += red[(k * T + j) * 64 + lane];
-        if (owns) out[pair_of(j) * hidden] = v;
+        if (owns) to[pair_of(j) * hidden] = v;
     }
 }
 
@@ -692,48 +831,57 @@ template <int BITS, int MAXQ>
 __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down(Projection down, Activations a,
                                                                       const int32_t *ids, int batch, int experts,
                                                                       int topk, int hidden, int inter, int parts,
-                                                                      float *partial)
+                                                                      int room, float *partial)
 {
     __shared__ ChosenLds chosen[kDefaultWaves];
-    extern __shared__ float red[];
+    extern __shared__ __align__(16) uint8_t space[];
     ChosenLds &lds = chosen[threadIdx.x >> 6];
     const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
     if (c.expert < 0) return;
     const int64_t pairs = batch * topk;
     if (MAXQ >= 4 && c.count > 8)
-        down_body<BITS, MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
+        down_body<BITS, MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
     else if (MAXQ >= 2 && c.count > 4)
-        down_body<BITS, MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
+        down_body<BITS, MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
     else if (MAXQ >= 1 && c.count > 2)
-        down_body<BITS, MAXQ >= 1 ? 2 : 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
+        down_body<BITS, MAXQ >= 1 ? 2 : 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
     else
-        down_body<BITS, 1>(down, a, lds, c, topk, hidden, inter, parts, pairs, partial, red);
+        down_body<BITS, 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
 }
 
-// y = the weighted sum of a token's partial sums, in the order of its choices;
-// a repeated id's partial sums stand at its first choice.
-__global__ void __launch_bounds__(256) experts_combine(const float *part, const int32_t *ids, const float *weights,
-                                                       int batch, int experts, int topk, int hidden, int splits,
-                                                       uint16_t *y)
+// y = the weighted sum of a token's partial sums, its choices in order; a
+// repeated id's partial sums stand at its first choice.  All of them are loaded
+// before the first is used.  (Adding them up in the down launch instead, by the
+// last workgroup of each 64 to 512 rows to arrive, measured slower at every
+// size: 14.4 us against 6.7 + 4.8 for one token and 6 experts of 2048x1280, 107
+// against 65 + 6 for 16 tokens and 128 experts.)
+__global__ void __launch_bounds__(256) experts_combine(const float *__restrict__ partial, const int32_t *__restrict__ ids,
+                                                       const float *__restrict__ weights, int batch, int experts,
+                                                       int topk, int hidden, int splits, uint16_t *__restrict__ y)
 {
     const int t = blockIdx.y, row = blockIdx.x * 256 + threadIdx.x;
-    float sum = 0.f;
-    for (int k = 0; k < topk; ++k) {
-        const int e = ids[t * topk + k];
-        if (e < 0 || e >= experts) continue;
-        float w = 0.f;
-        bool first = true;
+    const int64_t pairs = batch * topk;
+    const float *p = partial + (int64_t)t * topk * hidden + row;
+    float w[kMaxTopk], sum[kMaxTopk];
+#pragma unroll
+    for (int k = 0; k < kMaxTopk; ++k) {
+        const int e = k < topk ? ids[t * topk + k] : -1;
+        bool first = e >= 0 && e < experts;
+        w[k] = 0.f;
         for (int o = 0; o < topk; ++o)
             if (ids[t * topk + o] == e) {
                 if (o < k) first = false;
-                w += weights[t * topk + o];
+                w[k] += weights[t * topk + o];
             }
-        if (!first) continue;
-        float v = 0.f;
-        for (int s = 0; s < splits; ++s) v += part[((int64_t)s * batch * topk + t * topk + k) * hidden + row];
-        sum += w * v;
+        w[k] = first ? w[k] : 0.f;
+        sum[k] = 0.f;
+        if (first)
+            for (int s = 0; s < splits; ++s) sum[k] += p[(s * pairs + k) * hidden];
     }
-    y[(int64_t)t * hidden + row] = __builtin_bit_cast(uint16_t, (_Float16)sum);
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxTopk; ++k) v += w[k] * sum[k];
+    y[(int64_t)t * hidden + row] = __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
 // ---------------------------------------------------------------------------
@@ -862,6 +1010,8 @@ Projection projection(const sqllm_experts &p)
     return {(const uint8_t *)p.packed, p.lut, p.row_ptr, p.col_idx, p.val, p.nnz};
 }
 
+constexpr int64_t kStageRoom = 64 << 10;
+
 template <int BITS, int MAXQ>
 sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weights, const Projection &gate,
                       const Projection &up, const Projection &down, int batch, int experts, int topk, int hidden,
@@ -872,14 +1022,23 @@ sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weight
                            (float *)(ws + at.act + 4 * entries)};
     float *part = (float *)(ws + at.part);
     const int used = (int)used_at_most(batch, experts, topk), splits = down_splits(batch, experts, topk, hidden, inter);
+    // LDS of a workgroup: the waves' sums, or before that its tokens' activations
+    // for the outliers to gather from, if these take at most kStageRoom (two
+    // workgroups share a compute unit)
     const size_t red = (size_t)kDefaultWaves * 4 * MAXQ * 64 * sizeof(float);
+    auto space = [&](int64_t stage) { return std::max(red, (size_t)std::min(stage, kStageRoom)); };
+    const size_t gate_lds = space(gate.nnz + up.nnz > 0 ? (int64_t)batch * hidden * 2 : 0);
+    const size_t down_lds = space(down.nnz > 0 ? (int64_t)batch * inter * 4 : 0);
+    static std::atomic<uint64_t> gate_asked{0}, down_asked{0};
+    dev::raise_lds_limit((const void *)experts_gate_up<BITS, MAXQ>, gate_asked, (int)kStageRoom);
+    dev::raise_lds_limit((const void *)experts_down<BITS, MAXQ>, down_asked, (int)kStageRoom);
     const int down_parts = down_parts_for((int64_t)used * (hidden / 64) * splits, inter / splits);
     const int down_wgs = (hidden / 64 * down_parts + kDefaultWaves - 1) / kDefaultWaves;
     hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(inter / 64, used), dim3(64 * kDefaultWaves),
-                       red, stream, gate, up, x, ids, batch, experts, topk, hidden, inter, a);
+                       gate_lds, stream, gate, up, x, ids, batch, experts, topk, hidden, inter, (int)gate_lds, a);
     hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(down_wgs, used, splits),
-                       dim3(64 * kDefaultWaves), red, stream, down, a, ids, batch, experts, topk, hidden, inter,
-                       down_parts, part);
+                       dim3(64 * kDefaultWaves), down_lds, stream, down, a, ids, batch, experts, topk, hidden, inter,
+                       down_parts, (int)down_lds, part);
     hipLaunchKernelGGL(experts_combine, dim3(hidden / 256, batch), dim3(256), 0, stream, part, ids, weights, batch,
                        experts, topk, hidden, splits, y);
     return launched();

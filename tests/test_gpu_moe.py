@@ -18,7 +18,7 @@ pytestmark = pytest.mark.gpu
 class Proj:
     """One projection of every expert, on the host in 64 bits and on the device in the stored form."""
 
-    def __init__(self, experts, rows, cols, bits, seed, density=0.005, skew=False, lut_sigma=0.05):
+    def __init__(self, experts, rows, cols, bits, seed, density=0.005, skew=False, few=0, lut_sigma=0.05):
         r = np.random.default_rng(seed)
         codes = r.integers(0, 1 << bits, (experts, rows, cols), dtype=np.uint8)
         lut = np.sort(r.standard_normal((experts, rows, 1 << bits)) * lut_sigma, axis=2).astype(np.float16)
@@ -33,6 +33,9 @@ class Proj:
                 counts[:] = 0
                 counts[r.integers(0, counts.size, 3)] = cols // 2
                 counts[-1] = 5
+            if few:  # hardly any, among them the first and the last row's
+                counts[:] = 0
+                counts[[0, -1, -2][:few]] = 1
             row_ptr = np.concatenate([[0], np.cumsum(counts)])
             col = r.integers(0, cols, row_ptr[-1])  # repeated entries are summed
             val = (r.standard_normal(row_ptr[-1]) * 0.2).astype(np.float16)
@@ -115,7 +118,8 @@ def test_experts(bits, batch, experts, topk, hidden, inter):
 
 
 @pytest.mark.parametrize("bits", [2, 3, 4])
-@pytest.mark.parametrize("kw", [{"density": 0}, {"density": 0.05}, {"density": 0.01, "skew": True}])
+@pytest.mark.parametrize("kw", [{"density": 0}, {"density": 0.05}, {"density": 0.01, "skew": True},
+                                {"few": 1}, {"few": 3}])
 def test_outliers(bits, kw):
     step(f"moe outliers {bits}-bit {kw}")
     layer = Layer(3, 512, 768, bits, 11, **kw)
@@ -234,6 +238,23 @@ def test_route_ties_go_to_the_lowest_expert():
     zero = torch.zeros(4, 512, dtype=torch.float16, device="cuda")
     ids, weights = nw().moe_route(zero, router, 8, sigmoid=True)
     assert (ids.cpu() == torch.arange(8, dtype=torch.int32)).all() and (weights == 0.125).all()
+
+
+@pytest.mark.parametrize("offset", [-3000.0, 0.0, 700.0])
+def test_route_large_sums(offset):
+    """Sums whose exponentials over- and underflow by themselves; all of a token's sums negative."""
+    step(f"moe route offset {offset}")
+    x = torch.ones(2, 256, dtype=torch.float16, device="cuda")
+    router = tokens(100, 256, 2) * 0.1
+    router[:, 0] += offset
+    for sigmoid in (False, True):
+        ids, weights = nw().moe_route(x, router, 5, sigmoid=sigmoid, renormalize=False)
+        with np.errstate(over="ignore"):
+            rid, rw = route64(x, router, 5, sigmoid=sigmoid, renormalize=False)
+        if rw.min() > 1e-300 and rw.max() < 1:  # distinct scores
+            np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+        w = weights.cpu().numpy().astype(np.float64)
+        assert (np.abs(w - rw) <= 2.0 ** -22 * np.abs(rw) + 2.0 ** -149).all()
 
 
 def test_route_with_values_that_are_no_numbers():

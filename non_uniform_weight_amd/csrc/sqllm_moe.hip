@@ -859,24 +859,21 @@ __global__ void __launch_bounds__(256) experts_combine(const float *__restrict__
                                                        const float *__restrict__ weights, int batch, int experts,
                                                        int topk, int hidden, int splits, uint16_t *__restrict__ y)
 {
-    const int t = blockIdx.y, row = blockIdx.x * 256 + threadIdx.x;
+    const int t = blockIdx.y, row = blockIdx.x * 256 + threadIdx.x, lane = threadIdx.x & 63;
     const int64_t pairs = batch * topk;
     const float *p = partial + (int64_t)t * topk * hidden + row;
+    const int id = lane < topk ? ids[t * topk + lane] : -1; // lane k: choice k
+    const int weight = lane < topk ? __float_as_int(weights[t * topk + lane]) : 0;
     float w[kMaxTopk], sum[kMaxTopk];
 #pragma unroll
     for (int k = 0; k < kMaxTopk; ++k) {
-        const int e = k < topk ? ids[t * topk + k] : -1;
-        bool first = e >= 0 && e < experts;
-        w[k] = 0.f;
-        for (int o = 0; o < topk; ++o)
-            if (ids[t * topk + o] == e) {
-                if (o < k) first = false;
-                w[k] += weights[t * topk + o];
-            }
-        w[k] = first ? w[k] : 0.f;
-        sum[k] = 0.f;
-        if (first)
+        const int e = __builtin_amdgcn_readlane(id, k);
+        uint64_t same = __ballot(id == e);
+        w[k] = sum[k] = 0.f;
+        if (e >= 0 && e < experts && __builtin_ctzll(same) == k) {
             for (int s = 0; s < splits; ++s) sum[k] += p[(s * pairs + k) * hidden];
+            for (; same; same &= same - 1) w[k] += __int_as_float(__builtin_amdgcn_readlane(weight, __builtin_ctzll(same)));
+        }
     }
     float v = 0.f;
 #pragma unroll

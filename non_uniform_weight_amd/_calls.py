@@ -9,6 +9,7 @@ Small calls take a few microseconds on the GPU, so the checks here are the cheap
 from __future__ import annotations
 
 import functools
+import inspect
 import threading
 
 import torch
@@ -31,11 +32,17 @@ def device_of(x, name: str) -> int:
 
 def address(t, name: str, dtype, index: int) -> int:
     """Address of a contiguous tensor of this type on device `index`."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    return _checked_address(t, name, dtype, index)
+
+
+def _checked_address(t, name: str, dtype, index: int) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: torch.Tensor expected")
+    if t.get_device() < 0:
+        raise ValueError(f"{name}: device tensor expected (the operators run only on the GPU)")
     if t.get_device() != index:
-        if t.get_device() < 0:
-            raise ValueError(f"{name}: device tensor expected (the operators run only on the GPU)")
         raise ValueError(f"{name}: on {t.device}, the call's other tensors on cuda:{index}")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {dtype} expected, got {t.dtype}")
@@ -49,40 +56,50 @@ def output(t, name: str, shape: tuple, dtype, index: int):
     if t is None:
         t = torch.empty(shape, dtype=dtype, device=index)
         return t, t.data_ptr()
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {shape} expected, got {tuple(t.shape)}")
     return t, address(t, name, dtype, index)
 
 
+_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
 def on_stream(fn):
-    """Runs fn(..., index, handle) with the device of its first tensor current and its keyword `stream`, if given, as
+    """Runs fn(index, handle, ...) with the device of its first tensor current and its keyword `stream`, if given, as
     the current stream; handle is that stream's."""
+
+    # what a caller sees: fn's arguments but the first two, and stream
+    mine = inspect.signature(fn)
+    rest = [p for p in mine.parameters.values()][2:]
+    name = rest[0].name
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        index = device_of(args[0] if args else next(iter(kw.values()), None), fn.__name__)
+        index = device_of(args[0] if args else kw.get(name), name)
         if stream is not None:
             if stream.device.index != index:
                 raise ValueError(f"stream: on {stream.device}, the tensors on cuda:{index}")
             with torch.cuda.stream(stream):
-                return fn(*args, **kw, index=index, handle=stream.cuda_stream)
-        if torch._C._cuda_getDevice() != index:
+                return fn(index, stream.cuda_stream, *args, **kw)
+        if _device() != index:
             with torch.cuda.device(index):
-                return fn(*args, **kw, index=index, handle=torch._C._cuda_getCurrentRawStream(index))
-        return fn(*args, **kw, index=index, handle=torch._C._cuda_getCurrentRawStream(index))
+                return fn(index, _raw_stream(index), *args, **kw)
+        return fn(index, _raw_stream(index), *args, **kw)
 
+    call.__signature__ = mine.replace(parameters=[*rest, inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 
-def with_scratch(ws, nbytes: int, index: int, handle: int, launch) -> int:
-    """launch(address, bytes) with ws (uint8 tensor) or, if None, scratch of the current stream; its status."""
+def with_scratch(ws, nbytes: int, index: int, handle: int, fn, *args) -> int:
+    """fn(*args, address, bytes, handle) with ws (uint8 tensor) or, if None, scratch of the current stream."""
     if ws is not None:
-        return launch(address(ws, "workspace", torch.uint8, index), ws.numel())
-    if torch.cuda.is_current_stream_capturing():
+        return fn(*args, address(ws, "workspace", torch.uint8, index), ws.numel(), handle)
+    if torch._C._cuda_isCurrentStreamCapturing():
         ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=index)
-        return launch(ws.data_ptr(), ws.numel())
+        return fn(*args, ws.data_ptr(), ws.numel(), handle)
     with _LOCK:
         buf = _SCRATCH.get((index, handle))
-        if buf is None or buf.numel() < nbytes:
-            buf = _SCRATCH[index, handle] = torch.empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=index)
-        return launch(buf.data_ptr(), buf.numel())
+        if buf is None or buf[1] < nbytes:
+            ws = torch.empty(max(nbytes, 1 << 16), dtype=torch.uint8, device=index)
+            buf = _SCRATCH[index, handle] = (ws.data_ptr(), ws.numel(), ws)
+        return fn(*args, buf[0], buf[1], handle)

@@ -26,6 +26,7 @@ _lib.sqllm_fp8_gemm.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _sz, 
 
 EXPORTS = ("sqllm_fp8_cols", "sqllm_fp8_scale_pitch", "sqllm_fp8_quantize", "sqllm_fp8_workspace_bytes",
            "sqllm_fp8_gemm")
+_gemm = _lib.sqllm_fp8_gemm
 
 
 @functools.lru_cache(maxsize=4096)
@@ -46,7 +47,7 @@ def fp8_workspace_bytes(rows: int, cols: int, batch: int) -> int:
 
 
 @_calls.on_stream
-def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None, *, index, handle):
+def fp8_quantize(index, handle, x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
     """(q, scale) of fp16 x [rows, cols]; the columns of a row are adjacent, rows may be further apart than cols.
     Offline for weights; the product rounds its activations itself.  stream: as for every call (keyword)."""
     if x.dim() != 2 or x.numel() == 0:
@@ -64,8 +65,8 @@ def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Te
 
 
 @_calls.on_stream
-def fp8_gemm(q: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: torch.Tensor | None = None,
-             ws: torch.Tensor | None = None, *, index, handle) -> torch.Tensor:
+def fp8_gemm(index, handle, q: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: torch.Tensor | None = None,
+             ws: torch.Tensor | None = None) -> torch.Tensor:
     """y [batch, rows] = x W^T for fp16 x [batch, cols] (or [cols]) and W stored as fp8_quantize leaves it.
     ws: scratch of fp8_workspace_bytes(rows, cols, batch) bytes (a cached one if None)."""
     if not isinstance(x, torch.Tensor):
@@ -77,12 +78,12 @@ def fp8_gemm(q: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: torch.Ten
                          f"{tuple(q.shape)}")
     batch, cols = x.shape
     rows, kept = q.shape
-    if kept != fp8_cols(cols) or tuple(scale.shape) != (rows, fp8_scale_pitch(cols)):
+    if kept != fp8_cols(cols) or scale.shape != (rows, fp8_scale_pitch(cols)):
         raise ValueError(f"q, scale: shapes {(rows, fp8_cols(cols))} and {(rows, fp8_scale_pitch(cols))} expected for "
                          f"{cols} columns, got {tuple(q.shape)} and {tuple(scale.shape)}")
     qp, sp = _calls.address(q, "q", torch.uint8, index), _calls.address(scale, "scale", torch.uint8, index)
     xp = _calls.address(x, "x", torch.float16, index)
     y, yp = _calls.output(y, "y", (batch, rows), torch.float16, index)
-    _check(_calls.with_scratch(ws, fp8_workspace_bytes(rows, cols, batch), index, handle, lambda p, n: _lib.sqllm_fp8_gemm(
-        qp, sp, rows, cols, xp, batch, yp, p, n, handle)), "sqllm_fp8_gemm")
+    _check(_calls.with_scratch(ws, fp8_workspace_bytes(rows, cols, batch), index, handle, _gemm, qp, sp, rows, cols, xp,
+                               batch, yp), "sqllm_fp8_gemm")
     return y

@@ -34,6 +34,7 @@ _lib.sqllm_moe_layer.argtypes = [_vp, _vp, _vp, _i32, _f32, _ep, _ep, _ep, _i32,
 
 EXPORTS = ("sqllm_moe_workspace_bytes", "sqllm_moe_route", "sqllm_moe_experts", "sqllm_moe_layer")
 _SIGMOID, _KEEP_SUM = 1, 2
+_route, _experts, _layer = _lib.sqllm_moe_route, _lib.sqllm_moe_experts, _lib.sqllm_moe_layer
 
 
 @functools.lru_cache(maxsize=4096)
@@ -46,7 +47,7 @@ _packed_bytes = functools.lru_cache(maxsize=4096)(packed_bytes)
 
 def _projection(p, name, bits, rows, cols, experts, index) -> Experts:
     packed, lut = p["packed"], p["lut"]
-    if tuple(lut.shape) != (experts, rows, 1 << bits):
+    if lut.shape != (experts, rows, 1 << bits):
         raise ValueError(f"{name}.lut: shape {(experts, rows, 1 << bits)} expected, got {tuple(lut.shape)}")
     need = experts * _packed_bytes(rows, cols, bits)
     if packed.numel() < need or need == 0:
@@ -83,15 +84,15 @@ def _router(x, router, bias, index):
     experts = router.shape[0]
     if bias is None:
         return batch, hidden, experts, rp, None
-    if tuple(bias.shape) != (experts,):
+    if bias.shape != (experts,):
         raise ValueError(f"bias: shape {(experts,)} expected, got {tuple(bias.shape)}")
     return batch, hidden, experts, rp, _calls.address(bias, "bias", torch.float32, index)
 
 
 @_calls.on_stream
-def moe_route(x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tensor | None = None, sigmoid: bool = False,
+def moe_route(index, handle, x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tensor | None = None, sigmoid: bool = False,
               renormalize: bool = True, scale: float = 1.0, ids: torch.Tensor | None = None,
-              weights: torch.Tensor | None = None, ws: torch.Tensor | None = None, *, index, handle):
+              weights: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """(ids int32, weights fp32), both [batch, topk]: each token's experts by softmax (or sigmoid) scores of
     x router^T.  bias (fp32 [experts]) moves the choice only; renormalize divides a token's weights by their sum.
     stream: as for every call (keyword)."""
@@ -101,14 +102,14 @@ def moe_route(x: torch.Tensor, router: torch.Tensor, topk: int, bias: torch.Tens
     ids, ip = _calls.output(ids, "ids", (batch, topk), torch.int32, index)
     weights, wp = _calls.output(weights, "weights", (batch, topk), torch.float32, index)
     _check(_calls.with_scratch(
-        ws, moe_workspace_bytes(batch, experts, topk, hidden, 256), index, handle, lambda p, n: _lib.sqllm_moe_route(
-            xp, rp, bp, batch, experts, hidden, topk, flags, scale, ip, wp, p, n, handle)), "sqllm_moe_route")
+        ws, moe_workspace_bytes(batch, experts, topk, hidden, 256), index, handle, _route, xp, rp, bp, batch, experts,
+        hidden, topk, flags, scale, ip, wp), "sqllm_moe_route")
     return ids, weights
 
 
 @_calls.on_stream
-def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: dict, up: dict, down: dict, bits: int,
-                y: torch.Tensor | None = None, ws: torch.Tensor | None = None, *, index, handle) -> torch.Tensor:
+def moe_experts(index, handle, x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate: dict, up: dict, down: dict, bits: int,
+                y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """y [batch, hidden] = sum over a token's ids of weight * down(silu(gate x) * up x).  An id outside
     [0, experts) (-1 for a padded row) takes no part; a token without any gets zeros."""
     batch, hidden = _rows_of(x)
@@ -120,16 +121,16 @@ def moe_experts(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate:
     xp = _calls.address(x, "x", torch.float16, index)
     y, yp = _calls.output(y, "y", (batch, hidden), torch.float16, index)
     _check(_calls.with_scratch(
-        ws, moe_workspace_bytes(batch, experts, topk, hidden, inter), index, handle, lambda p, n: _lib.sqllm_moe_experts(
-            xp, ip, wp, g, u, d, bits, batch, experts, topk, hidden, inter, yp, p, n, handle)), "sqllm_moe_experts")
+        ws, moe_workspace_bytes(batch, experts, topk, hidden, inter), index, handle, _experts, xp, ip, wp, g, u, d, bits,
+        batch, experts, topk, hidden, inter, yp), "sqllm_moe_experts")
     return y
 
 
 @_calls.on_stream
-def moe_layer(x: torch.Tensor, router: torch.Tensor, topk: int, gate: dict, up: dict, down: dict, bits: int,
+def moe_layer(index, handle, x: torch.Tensor, router: torch.Tensor, topk: int, gate: dict, up: dict, down: dict, bits: int,
               bias: torch.Tensor | None = None, sigmoid: bool = False, renormalize: bool = True, scale: float = 1.0,
               y: torch.Tensor | None = None, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
-              ws: torch.Tensor | None = None, *, index, handle):
+              ws: torch.Tensor | None = None):
     """(y, ids, weights): moe_route and moe_experts in one call."""
     batch, hidden, experts, rp, bp = _router(x, router, bias, index)
     inter = gate["lut"].shape[1]
@@ -140,7 +141,6 @@ def moe_layer(x: torch.Tensor, router: torch.Tensor, topk: int, gate: dict, up: 
     ids, ip = _calls.output(ids, "ids", (batch, topk), torch.int32, index)
     weights, wp = _calls.output(weights, "weights", (batch, topk), torch.float32, index)
     _check(_calls.with_scratch(
-        ws, moe_workspace_bytes(batch, experts, topk, hidden, inter), index, handle, lambda p, n: _lib.sqllm_moe_layer(
-            xp, rp, bp, flags, scale, g, u, d, bits, batch, experts, topk, hidden, inter, ip, wp, yp, p, n, handle)),
-        "sqllm_moe_layer")
+        ws, moe_workspace_bytes(batch, experts, topk, hidden, inter), index, handle, _layer, xp, rp, bp, flags, scale, g, u,
+        d, bits, batch, experts, topk, hidden, inter, ip, wp, yp), "sqllm_moe_layer")
     return y, ids, weights

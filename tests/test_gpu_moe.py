@@ -291,6 +291,14 @@ def test_layer_is_the_two_calls(small, batch):
     small.check(x, ids, weights, y)
 
 
+def test_arguments_by_name(small):
+    step("moe arguments by name")
+    x, router = tokens(2, 512, 41), make_router(small, 42)
+    parts = dict(gate=small.gate.dev, up=small.up.dev, down=small.down.dev, bits=3)
+    y, ids, weights = nw().moe_layer(topk=2, router=router, x=x, **parts)
+    assert torch.equal(y, nw().moe_experts(weights=weights, ids=ids, x=x, **parts))
+
+
 def test_own_workspace_with_any_contents(small):
     step("moe workspace")
     x, router = tokens(9, 512, 41), make_router(small, 42)

@@ -20,9 +20,10 @@
  * Arithmetic: router sums, scores and the comparison in 64 bits, so that the
  * choice does not depend on the order of a sum.  Expert products of two fp16
  * values are summed in fp32; a is stored as an unevaluated sum of two fp16
- * values (about 22 bits), the form in which the matrix cores take it; y is
- * rounded once.  Sums are taken in a fixed order: repeated calls
- * give identical bits.
+ * values, hi + lo * 2^-11, the form in which the matrix cores take it: 22
+ * bits, or 2^-36 where |a| < 2^-14, and infinite from 65520 on, as an fp16
+ * activation would be; y is rounded once.  Sums are taken in a fixed order:
+ * repeated calls give identical bits.
  *
  * Shapes: 1 <= batch <= 16; 1 <= experts <= 512; 1 <= topk <= min(8,
  * experts); hidden and inter multiples of 256 in [256, 65536]; experts *

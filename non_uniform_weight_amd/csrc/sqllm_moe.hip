@@ -45,7 +45,8 @@ __device__ __forceinline__ void row_sums(const uint16_t *const (&w)[R], const ui
     for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int t = 0; t < T; ++t) sum[r][t] = 0.0;
-#pragma unroll(R * T > 1 ? 2 : 4)
+    constexpr int kAtOnce = R * T > 1 ? 2 : 4;
+#pragma unroll kAtOnce
     for (int c = lane * 8; c < hidden; c += 512) {
         half8_t wv[R], xv[T];
 #pragma unroll
@@ -695,7 +696,8 @@ __device__ __forceinline__ void stage_rows(int rows, int bytes, S source, uint8_
 
 // ---------------------------------------------------------------------------
 // a = silu(gate x) * (up x), split into two fp16 values per entry for the
-// matrix steps of down (storing a in one would double the error of y) and
+// matrix steps of down, hi + lo * 2^-11 (one fp16 value would double the error
+// of y; without the factor lo would have no bits left where a is small), and
 // whole for its outliers.
 // The even waves of a workgroup have the gate's tile, the odd ones the up's.
 // (Two or four tiles to a workgroup, with two or four of its waves each,
@@ -747,7 +749,7 @@ __device__ __forceinline__ void gate_up_body(const Projection &gate, const Proje
         }
         const float v = g / (1.f + expf(-g)) * u;
         const _Float16 hi = (_Float16)v;
-        const float rest = fabsf(v) < 65520.f ? v - (float)hi : 0.f; // beyond, hi is infinite or NaN already
+        const float rest = fabsf(v) < 65520.f ? (v - (float)hi) * 2048.f : 0.f; // beyond, hi is infinite or NaN
         const int64_t pair = (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8);
         const int64_t at = pair * inter + t * 64 + lane;
         a.hi[at] = __builtin_bit_cast(uint16_t, hi);
@@ -809,15 +811,16 @@ __device__ __forceinline__ void down_body(const Projection &down, Activations a,
     } else if (down.nnz > 0) {
         out.add<T>(c.count, [&](int j, int col) { return whole_of(j)[col]; }, sum);
     }
+    auto whole = [&](int j) { return sum[j] + sum[T + j] * 0x1p-11f; };
     float *const red = (float *)space;
     if (parts == 1) {
 #pragma unroll
         for (int j = 0; j < T; ++j)
-            if (owns && j < c.count) to[pair_of(j) * hidden] = sum[j] + sum[T + j];
+            if (owns && j < c.count) to[pair_of(j) * hidden] = whole(j);
         return;
     }
 #pragma unroll
-    for (int j = 0; j < T; ++j) red[(w * T + j) * 64 + lane] = sum[j] + sum[T + j];
+    for (int j = 0; j < T; ++j) red[(w * T + j) * 64 + lane] = whole(j);
     __syncthreads();
     const int w0 = w - part;
     for (int j = part; j < c.count; j += parts) {
@@ -915,7 +918,9 @@ int down_parts_for(int64_t tiles, int64_t inter)
 
 // Workgroups that share a down tile's columns: more than one only while the
 // launch would leave compute units without work and every wave keeps at
-// least two half groups.
+// least two half groups (one, two and four splits, us of the whole call: one
+// token, 2 of 8 experts 2048x5632 at 4 bits 29.8, 25.3, 24.9; 4 of 60 experts
+// 2048x1536 15.9, 16.5, 20.4).
 int down_splits(int batch, int experts, int topk, int64_t hidden, int64_t inter)
 {
     int s = 1;
@@ -975,7 +980,12 @@ sqllm_status check_products(const uint16_t *x, const int32_t *ids, const float *
     return SQLLM_OK;
 }
 
-constexpr int64_t kRouteSmall = 131072; // experts * hidden up to which one launch routes
+// experts * hidden up to which one launch routes.  On the GPU one launch takes
+// longer, since a token's workgroup reads the whole router through one compute
+// unit's loads (8 experts of 4096: 5.3 us against 4.9 in two launches, 64 of
+// 2048 7.3 against 4.2, 64 of 4096 11.6 against 5.0), but the second launch
+// costs the host about 3.6 us, which is what bounds small layers.
+constexpr int64_t kRouteSmall = 131072;
 
 sqllm_status launched() { return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP; }
 
@@ -1007,6 +1017,9 @@ Projection projection(const sqllm_experts &p)
     return {(const uint8_t *)p.packed, p.lut, p.row_ptr, p.col_idx, p.val, p.nnz};
 }
 
+// 64 KB (16 tokens, 8 experts 4096x3584 at 4 bits: 70 us a call against 75
+// with 32 KB, where fewer experts' tokens fit, and 76 gathering from memory;
+// 16 tokens, 128 experts 4096x1536: 146, 147 and 150).
 constexpr int64_t kStageRoom = 64 << 10;
 
 template <int BITS, int MAXQ>

@@ -58,7 +58,7 @@ class Layer:
     def run(self, x, ids, weights, **kw):
         return nw().moe_experts(x, ids, weights, self.gate.dev, self.up.dev, self.down.dev, self.bits, **kw)
 
-    def check(self, x, ids, weights, y):
+    def check(self, x, ids, weights, y, floor=2.0 ** -25):
         x64, w64 = x.cpu().numpy().astype(np.float64), weights.cpu().numpy().astype(np.float64)
         ids, y = ids.cpu().numpy(), y.float().cpu().numpy().astype(np.float64)
         eps = 2.0 ** -23
@@ -75,7 +75,7 @@ class Layer:
                 dg, du = self.gate.n[e] * eps * (self.gate.abs[e] @ av), self.up.n[e] * eps * (self.up.abs[e] @ av)
                 s = g / (1 + np.exp(-g))
                 a = s * u
-                da = 1.1 * np.abs(u) * dg + np.abs(s) * du + 2.0 ** -19 * np.abs(a) + 2.0 ** -25
+                da = 1.1 * np.abs(u) * dg + np.abs(s) * du + 2.0 ** -19 * np.abs(a) + floor
                 down = self.down.abs[e]
                 ref += w64[t, k] * (self.down.dense[e] @ a)
                 err += abs(w64[t, k]) * (down @ da + self.down.n[e] * eps * (down @ np.abs(a)))
@@ -127,6 +127,20 @@ def test_outliers(bits, kw):
         x = tokens(batch, 512, 3)
         ids, weights = choices(batch, 3, 2, 4)
         layer.check(x, ids, weights, layer.run(x, ids, weights))
+
+
+@pytest.mark.parametrize("density", [0, 0.005])
+def test_small_activations(density):
+    """Entries of a around 2^-17, below fp16's normal range, with weights that lift y well above it: they are stored
+    to 2^-36, and what the fp32 sums of gate and up are off by is far smaller still."""
+    step("moe small activations")
+    layer = Layer(3, 512, 768, 3, 23, density=density)
+    x = tokens(5, 512, 5) / 256
+    ids, weights = choices(5, 3, 2, 6)
+    weights *= 4096
+    y = layer.run(x, ids, weights)
+    assert y.float().abs().median() > 2.0 ** -8
+    layer.check(x, ids, weights, y, floor=2.0 ** -36)
 
 
 def test_outliers_in_one_projection_only():

@@ -41,7 +41,7 @@ int64_t sqllm_fp8_scale_pitch(int64_t cols);
 /*
  * sqllm_fp8_quantize -- fp16 values to the stored form.
  *   x: fp16, row r at x + r * ldx (ldx >= cols, in values), 2-byte aligned;
- *   1 <= rows < 2^31, 1 <= cols <= 2^24, rows * scale pitch < 2^30 (else
+ *   rows >= 1, 1 <= cols <= 2^24, rows * scale pitch <= 2^30 - 256 (else
  *   SQLLM_ERR_SHAPE).
  */
 sqllm_status sqllm_fp8_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, uint8_t *q,
@@ -61,8 +61,9 @@ size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
  * its own rounding.  A value of x that is infinite or NaN makes its row of y
  * NaN.
  *   x: 2-byte aligned, contiguous; y: fp16 [batch][rows], 2-byte aligned,
- *   must not overlap an input; 1 <= batch < 2^31 (else SQLLM_ERR_BATCH);
- *   the bounds of sqllm_fp8_quantize hold for both matrices.
+ *   must not overlap an input.  The bounds of sqllm_fp8_quantize hold for both
+ *   matrices (else SQLLM_ERR_BATCH for x) and rows * batch <= 2^38 (else
+ *   SQLLM_ERR_SHAPE).
  */
 sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols, const uint16_t *x,
                             int64_t batch, uint16_t *y, void *workspace, size_t workspace_bytes, hipStream_t stream);

@@ -647,11 +647,15 @@ __global__ void __launch_bounds__(64 * kStreamWaves, 4) gemm_stream(Operands p, 
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
+// Within these, counts of tiles fit 32 bits and so do the work-items of every
+// launch (a launch takes no more), and word indices of scales 32 bits.
 bool good_shape(int64_t rows, int64_t cols)
 {
     return rows >= 1 && rows <= INT32_MAX && cols >= 1 && cols <= kMaxCols &&
-           rows * sqllm_fp8_scale_pitch(cols) <= INT32_MAX / 2;
+           rows * sqllm_fp8_scale_pitch(cols) <= ((int64_t)1 << 30) - 256;
 }
+
+bool good_product(int64_t rows, int64_t batch) { return rows * batch <= (int64_t)1 << 38; }
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -673,12 +677,18 @@ void launch_add(const Operands &p, int splits, const float *partial, hipStream_t
                        p.y);
 }
 
-// Splits of a streamed product's columns: while few rows give half of the
-// compute units no workgroup and every wave keeps at least eight blocks.
+// Splits of a streamed product's columns, up to 256 workgroups in all and two
+// blocks a wave at least.  Adding the sums up is a launch more, about 3.6 us of
+// the host's time, so only where the rows are few enough for it to save that
+// (batch 1 and 16, us at 1, 2, 4 and 8 splits: 256x8192 9.7, 8.8, 7.7, 8.4 and
+// 17, 15, 12, 13; 1024x16384 17, 14, 12, 13 and 25, 20, 17, 18; 2048x16384 18,
+// 17, 19, 20 and 27, 22, 26, 28; but 2048x8192 11, 11, 12, 17 and 18, 16, 17,
+// 26).
 int stream_splits(int64_t rows, int64_t blocks)
 {
+    if (blocks < 64 || rows > 16 * blocks) return 1;
     int s = 1;
-    while (s < 8 && rows * s <= 16 * 128 && blocks >= 2 * s * 8 * kStreamWaves) s *= 2;
+    while (s < 8 && rows * s < 16 * 256 && blocks >= 4 * s * kStreamWaves) s *= 2;
     return s;
 }
 
@@ -715,8 +725,24 @@ void launch_large(const Operands &p, hipStream_t stream)
     hipLaunchKernelGGL(gemm_large, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(512), kUnits * kUnit, stream, p);
 }
 
-// The tiling of a product: the tile of x rows by the batch, W rows by how many
-// workgroups that gives, and splits of the columns where they are too few.
+// The tiling of a product: the largest tile that still gives most compute
+// units a workgroup, and splits of the columns where no tile does.  Measured,
+// in us:
+//   256x256 (gemm_large) against 128x128: 6144x8192 at batch 2048 (192 tiles
+//     of 256) 112 and 147, 4096x8192 at 2816 (176) 121 and 132, 8192x8192 at
+//     1024 (128) 107 and 100, 4096x4096 at 2048 (128) 62 and 49.
+//   128x128 against 64x64: 4096x4096 at 768 (192 tiles of 128) 41 and 42, at
+//     512 (128) 41 and 30; 12288x4096 at 256 (192) 41 and 43; 8192x8192 at 512
+//     (256) 73 and 101, at 200 (128) 70 and 44.
+//   64x64 against 64x32: 4096x4096 at 200 (256 tiles of 64) 17 and 21, at 96
+//     (128) 16.4 and 15.3; 8192x8192 at 96 (256) 30 and 45.
+//   One, two and four splits of 64x32 tiles: 4096x4096 at 20 (64 tiles) 14.3,
+//     13.3, 12.3, at 96 (192) 15, 20, 22; 2048x8192 at 128 (128) 25, 19, 21;
+//     1000x2048 at 20 (16) 9.4, 10.0, 9.6.
+// From 16384 columns on, a split's sums cost little beside its products, and
+// splits of a larger tile read less than small tiles do: 4096x16384 at 256
+// 57 us with 128x128 in four splits, 71 with 64x64, 92 with 64x32; at 768 101
+// with 128x128 in two splits, 131 in one, 164 with 64x64.
 struct Choice {
     int tile; // of launch below
     int splits;
@@ -726,17 +752,19 @@ Choice choose(int64_t rows, int64_t cols, int64_t batch)
 {
     const int64_t blocks = sqllm_fp8_cols(cols) / kBlock;
     auto tiles = [&](int tm, int tn) { return ((rows + tm - 1) / tm) * ((batch + tn - 1) / tn); };
-    if (batch > 256 && tiles(256, 256) >= 192) return Choice{0, 1};
+    if (batch > 256 && tiles(256, 256) >= 160) return Choice{0, 1};
+    const bool deep = blocks >= 128;
+    const int64_t enough = deep ? 256 : 192;
     Choice c;
     int64_t wgs;
-    if (batch > 64)
+    if (batch > 64 && (deep || tiles(128, 128) >= enough))
         c.tile = 1, wgs = tiles(128, 128);
-    else if (batch > 32)
+    else if (batch > 32 && (deep || tiles(64, 64) >= enough))
         c.tile = 2, wgs = tiles(64, 64);
     else
         c.tile = 3, wgs = tiles(64, 32);
-    int64_t s = 1;
-    while (s < 8 && wgs * s < 256 && blocks >= 16 * s) s *= 2;
+    int64_t s = 1; // no split below eight blocks
+    while (s < 8 && wgs * s < enough && blocks >= 32 && blocks >= 16 * s) s *= 2;
     const int64_t share = (blocks + s - 1) / s;
     c.splits = (int)((blocks + share - 1) / share); // none empty
     return c;
@@ -777,7 +805,7 @@ extern "C" sqllm_status sqllm_fp8_quantize(const uint16_t *x, int64_t rows, int6
 
 extern "C" size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
 {
-    if (!good_shape(rows, cols) || batch < 1 || !good_shape(batch, cols)) return 0;
+    if (!good_shape(rows, cols) || !good_shape(batch, cols) || !good_product(rows, batch)) return 0;
     const int splits = batch <= 16 ? stream_splits(rows, sqllm_fp8_cols(cols) / kBlock) : choose(rows, cols, batch).splits;
     return up256((size_t)batch * sqllm_fp8_cols(cols)) + up256((size_t)batch * sqllm_fp8_scale_pitch(cols)) +
            (splits > 1 ? (size_t)splits * batch * rows * 4 : 0);
@@ -789,7 +817,8 @@ extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, i
 {
     if (!q || !scale || !x || !y) return SQLLM_ERR_NULL;
     if (!good_shape(rows, cols)) return SQLLM_ERR_SHAPE;
-    if (batch < 1 || !good_shape(batch, cols)) return SQLLM_ERR_BATCH;
+    if (!good_shape(batch, cols)) return SQLLM_ERR_BATCH;
+    if (!good_product(rows, batch)) return SQLLM_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(scale, 4) || !aligned(x, 2) || !aligned(y, 2)) return SQLLM_ERR_ALIGN;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < sqllm_fp8_workspace_bytes(rows, cols, batch))
         return SQLLM_ERR_WORKSPACE;
@@ -798,17 +827,18 @@ extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, i
                         (int)sqllm_fp8_scale_pitch(cols)};
     float *partial = (float *)(xs + up256((size_t)batch * sqllm_fp8_scale_pitch(cols)));
     // A small matrix for a few rows of x: one launch that rounds x as it goes
-    // (4096x4096 at batch 1: 8.3 us against 2.2 and 6.5 in two launches, at
-    // batch 16 13.6 against 3.3 and 10.8).
-    if (batch <= 8 && rows * cols <= 1 << 24 && aligned(x, 16) && cols % 8 == 0) {
+    // (4096x4096 at batch 1, 8 and 16: 8.7, 10.3 and 13.2 us against 9.6, 11.7
+    // and 13.9 in two launches; 8192x4096 13.8, 17.5 and 23.1 against 13.2, 14.5
+    // and 15.9).
+    if (batch <= 16 && rows * cols <= 1 << 24 && aligned(x, 16) && cols % 8 == 0) {
         launch_stream<1, true>(p, x, (int)cols, partial, stream);
         return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
     }
     const sqllm_status st = quantize(x, batch, cols, cols, xq, xs, stream);
     if (st != SQLLM_OK) return st;
     // Two groups of 16 rows a wave halve the reads of x, where there are rows
-    // enough (8192x22016: 33 us either way at batch 1, 39 against 46 at batch
-    // 16; 4096x4096: 7.7 against 6.5).
+    // enough (8192x8192 at batch 1 and 16: 21.1 and 23.1 us against 20.2 and
+    // 30.1 with one group; 4096x8192: 15.1 and 19.0 against 12.8 and 18.3).
     if (batch <= 16 && rows >= 8192)
         launch_stream<2, false>(p, x, (int)cols, partial, stream);
     else if (batch <= 16)

@@ -59,6 +59,9 @@ def test_fp8_argument_errors(lib):
         assert gemm(lib, **{name: None}) == 1
     assert gemm(lib, rows=0) == gemm(lib, cols=-1) == gemm(lib, rows=1 << 29) == 3
     assert gemm(lib, batch=0) == gemm(lib, batch=1 << 29) == 4
+    assert quantize(lib, rows=(1 << 28) - 63, cols=5, ldx=5) == gemm(lib, rows=(1 << 28) - 63, cols=5) == 3
+    assert gemm(lib, rows=1 << 20, batch=1 << 19) == 3  # more of y than the launches count
+    assert lib.sqllm_fp8_workspace_bytes(1 << 20, 300, 1 << 19) == 0
     assert gemm(lib, q=P(0x100008)) == gemm(lib, scale=P(0x100002)) == gemm(lib, x=ODD) == gemm(lib, y=ODD) == 5
     assert gemm(lib, ws=None) == gemm(lib, ws=P(0x100010)) == gemm(lib, wsb=16) == 8
 

@@ -670,6 +670,105 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
         for (int r = 0; r < 4; ++r) sum[4 * h + r] = C == 2 ? acc[h][0][r] + acc[h][C - 1][r] : acc[h][0][r];
 }
 
+// The other decode, at 4 bits: a table in LDS of the tile's pairs of centroids,
+// entry [second code][first code][row] of two fp16 values (64 KB; a row's
+// entries share a bank of its own).  A pair of codes is a byte, and the address
+// of its entry that byte above the row's: one v_perm_b32 and one LDS read for
+// two weights, in the order of their columns, where the decode from registers
+// takes six vector instructions.
+constexpr int kPairTable = 256 * 64 * 4;
+
+// A row's centroids, and those of the two second codes whose entries this wave
+// writes.
+struct PairRow {
+    uint32_t first[8], second;
+
+    __device__ __forceinline__ void load(const uint16_t *row, int wave)
+    {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const u32x4 v = ((const u32x4 *)row)[q];
+            first[4 * q] = v.x, first[4 * q + 1] = v.y, first[4 * q + 2] = v.z, first[4 * q + 3] = v.w;
+        }
+        second = ((const uint32_t *)row)[wave];
+    }
+
+    __device__ __forceinline__ void store(uint8_t *table, int wave) const
+    {
+        static_assert(kDefaultWaves == 8, "two of the sixteen second codes a wave");
+        uint32_t *to = (uint32_t *)table + wave * (2 * 16 * 64) + (threadIdx.x & 63);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+                to[(s * 16 + c) * 64] =
+                    perm(second, first[c / 2], (c & 1 ? 0x0302 : 0x0100) | (s ? 0x07060000 : 0x05040000));
+    }
+};
+
+// A ring of a wave's half groups on their way, D of them: codes and
+// activations; and the sums of one matrix.
+template <int NQ>
+struct TableProduct {
+    static constexpr int D = NQ == 4 ? 1 : 2, C = NQ == 1 ? 2 : 1;
+    Half<4> codes[D];
+    u32x4 x[D][NQ];
+    f32x4 acc[NQ][C];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int h = 0; h < NQ; ++h)
+#pragma unroll
+            for (int c = 0; c < C; ++c) acc[h][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+
+    // Half group g (128 columns) of a tile into slot k; g < 0: zeros, so that
+    // every step issues the same loads.
+    __device__ __forceinline__ void load(int k, const uint8_t *tile, const uint16_t *const (&rows)[NQ], int g)
+    {
+        const int lane = threadIdx.x & 63;
+        codes[k].load((g >= 0 ? tile + (int64_t)g * (4 * 1024) : (const uint8_t *)dev::g_placeholder) + lane * 16);
+#pragma unroll
+        for (int h = 0; h < NQ; ++h)
+            x[k][h] = *(const u32x4 *)((g >= 0 ? rows[h] + 128 * g : (const uint16_t *)dev::g_placeholder) + 8 * (lane >> 2));
+    }
+
+    __device__ __forceinline__ void multiply(int k, const uint8_t *table)
+    {
+        const uint32_t row = (threadIdx.x & 63) * 4; // of an entry, below the pair's byte
+        [&]<int... Ns>(std::integer_sequence<int, Ns...>) {
+            (
+                [&] {
+                    const uint32_t v = codes[k].template pairs<Ns>();
+                    const uint32_t e0 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0400));
+                    const uint32_t e1 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0500));
+                    const uint32_t e2 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0600));
+                    const uint32_t e3 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0700));
+#pragma unroll
+                    for (int h = 0; h < NQ; ++h)
+                        acc[h][0] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2{x[k][h].x, x[k][h].y}),
+                                                                      __builtin_bit_cast(half4_t, u32x2{e0, e1}), acc[h][0], 4,
+                                                                      Ns, 0);
+#pragma unroll
+                    for (int h = 0; h < NQ; ++h)
+                        acc[h][C - 1] = __builtin_amdgcn_mfma_f32_4x4x4f16(
+                            __builtin_bit_cast(half4_t, u32x2{x[k][h].z, x[k][h].w}),
+                            __builtin_bit_cast(half4_t, u32x2{e2, e3}), acc[h][C - 1], 4, Ns, 0);
+                }(),
+                ...);
+        }(std::make_integer_sequence<int, 16>{});
+    }
+
+    __device__ __forceinline__ void sums(float (&sum)[4 * NQ]) const
+    {
+#pragma unroll
+        for (int h = 0; h < NQ; ++h)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[4 * h + r] = C == 2 ? acc[h][0][r] + acc[h][C - 1][r] : acc[h][0][r];
+    }
+};
+
 // Every wave's loads into LDS have arrived.
 __device__ __forceinline__ void all_loads_done()
 {
@@ -710,6 +809,19 @@ struct Activations { // [pair][inter]
     float *whole;
 };
 
+__device__ __forceinline__ void store_activation(const Activations &a, const ChosenLds &lds, int j, int topk, int inter,
+                                                 int tile, float g, float u)
+{
+    const float v = g / (1.f + expf(-g)) * u;
+    const _Float16 hi = (_Float16)v;
+    const float rest = fabsf(v) < 65520.f ? (v - (float)hi) * 2048.f : 0.f; // beyond, hi is infinite or NaN
+    const int64_t pair = (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8);
+    const int64_t at = pair * inter + tile * 64 + (threadIdx.x & 63);
+    a.hi[at] = __builtin_bit_cast(uint16_t, hi);
+    a.lo[at] = __builtin_bit_cast(uint16_t, (_Float16)rest);
+    a.whole[at] = v;
+}
+
 template <int BITS, int NQ>
 __device__ __forceinline__ void gate_up_body(const Projection &gate, const Projection &up, const uint16_t *x,
                                              const ChosenLds &lds, Chosen c, int topk, int hidden, int inter,
@@ -747,15 +859,118 @@ __device__ __forceinline__ void gate_up_body(const Projection &gate, const Proje
             g += red[(k * 4 * NQ + j) * 64 + lane];
             u += red[((k + 1) * 4 * NQ + j) * 64 + lane];
         }
-        const float v = g / (1.f + expf(-g)) * u;
-        const _Float16 hi = (_Float16)v;
-        const float rest = fabsf(v) < 65520.f ? (v - (float)hi) * 2048.f : 0.f; // beyond, hi is infinite or NaN
-        const int64_t pair = (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8);
-        const int64_t at = pair * inter + t * 64 + lane;
-        a.hi[at] = __builtin_bit_cast(uint16_t, hi);
-        a.lo[at] = __builtin_bit_cast(uint16_t, (_Float16)rest);
-        a.whole[at] = v;
+        store_activation(a, lds, j, topk, inter, t, g, u);
     }
+}
+
+// The same by pair tables: all waves have the gate's tile, then the up's, each
+// at every eighth half group, in one stream of loads; the up's table takes the
+// gate's place, so that two workgroups share a compute unit.
+template <int NQ>
+__device__ __forceinline__ void gate_up_table_body(const Projection &gate, const Projection &up, const uint16_t *x,
+                                                   const ChosenLds &lds, Chosen c, int topk, int hidden, int inter,
+                                                   int room, Activations a, uint8_t *space)
+{
+    using Product = TableProduct<NQ>;
+    constexpr int D = Product::D;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int t = blockIdx.x;
+    const int64_t tile = (int64_t)c.expert * (inter >> 6) + t, row = tile * 64 + lane;
+    auto row_of = [&](int j) { return x + (int64_t)(lds.list[j] & 255) * hidden; };
+    PairRow first, second;
+    first.load(gate.lut + row * 16, w);
+    second.load(up.lut + row * 16, w);
+    const int32_t *grp = gate.nnz ? gate.row_ptr + row : (const int32_t *)dev::g_placeholder;
+    const int32_t *urp = up.nnz ? up.row_ptr + row : (const int32_t *)dev::g_placeholder;
+    const int g_lo = grp[0], g_hi = grp[1], u_lo = urp[0], u_hi = urp[1];
+    const int halves = hidden >> 7, n = max(0, (halves - w + kDefaultWaves - 1) / kDefaultWaves); // of this wave
+    const int steps = (n + D - 1) / D * D;
+    const int64_t from = tile * halves * (4 * 1024);
+    const uint16_t *xr[NQ];
+#pragma unroll
+    for (int h = 0; h < NQ; ++h) xr[h] = row_of(min(4 * h + (lane & 3), c.count - 1)); // past the last: a copy, dropped
+    Product p;
+    auto load = [&](int k, int i) { // gate's steps, then up's
+        const int at = i < steps ? i : i - steps;
+        p.load(k, (i < steps ? gate : up).packed + from, xr, at < n ? w + at * kDefaultWaves : -1);
+    };
+    auto run = [&](int first) {
+        p.clear();
+        for (int i = first; i < first + steps; i += D) {
+#pragma unroll
+            for (int k = 0; k < D; ++k) {
+                p.multiply(k, space);
+                load(k, i + k + D);
+            }
+        }
+    };
+    float sum[2][4 * NQ];
+#pragma unroll
+    for (int k = 0; k < D; ++k) load(k, k);
+    first.store(space, w);
+    dev::lds_barrier();
+    run(0);
+    p.sums(sum[0]);
+    dev::lds_barrier(); // the gate's table is done with
+    second.store(space, w);
+    dev::lds_barrier();
+    run(steps);
+    p.sums(sum[1]);
+    __syncthreads(); // the up's too
+    if (gate.nnz + up.nnz > 0) {
+        const bool staged = c.count * hidden * 2 <= room;
+        if (staged) {
+            stage_rows(c.count, hidden * 2, [&](int j) { return (const uint8_t *)row_of(j); }, space);
+            all_loads_done();
+        }
+        const uint16_t *xs = (const uint16_t *)space;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Projection &q = s ? up : gate;
+            if (q.nnz == 0) continue;
+            Outliers out;
+            out.set(q, s ? u_lo : g_lo, s ? u_hi : g_hi, w, kDefaultWaves);
+            if (staged)
+                out.add<4 * NQ>(c.count, [&](int j, int col) { return dev::f16_to_f32(xs[j * hidden + col]); }, sum[s]);
+            else
+                out.add<4 * NQ>(c.count, [&](int j, int col) { return dev::f16_to_f32(row_of(j)[col]); }, sum[s]);
+        }
+        __syncthreads(); // the space is used again below
+    }
+    float *const red = (float *)space;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < 4 * NQ; ++j) red[((s * kDefaultWaves + w) * 4 * NQ + j) * 64 + lane] = sum[s][j];
+    __syncthreads();
+    for (int j = w; j < c.count; j += kDefaultWaves) {
+        float g = 0.f, u = 0.f;
+#pragma unroll
+        for (int k = 0; k < kDefaultWaves; ++k) {
+            g += red[(k * 4 * NQ + j) * 64 + lane];
+            u += red[((kDefaultWaves + k) * 4 * NQ + j) * 64 + lane];
+        }
+        store_activation(a, lds, j, topk, inter, t, g, u);
+    }
+}
+
+template <int MAXQ>
+__global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up_table(Projection gate, Projection up,
+                                                                        const uint16_t *x, const int32_t *ids, int batch,
+                                                                        int experts, int topk, int hidden, int inter,
+                                                                        int room, Activations a)
+{
+    __shared__ ChosenLds chosen[kDefaultWaves];
+    extern __shared__ __align__(16) uint8_t space[];
+    ChosenLds &lds = chosen[threadIdx.x >> 6];
+    const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
+    if (c.expert < 0) return;
+    if (MAXQ >= 4 && c.count > 8)
+        gate_up_table_body<MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
+    else if (MAXQ >= 2 && c.count > 4)
+        gate_up_table_body<MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
+    else
+        gate_up_table_body<1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
 }
 
 template <int BITS, int MAXQ>
@@ -782,6 +997,96 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Project
 // share a tile and split.
 // Grid (ceil(hidden / 64 / (8 / parts)), experts in use at most, splits).
 // ---------------------------------------------------------------------------
+template <int NQ>
+__device__ __forceinline__ void down_table_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
+                                                int topk, int hidden, int inter, int room, int64_t pairs,
+                                                float *partial, uint8_t *space)
+{
+    using Product = TableProduct<NQ>;
+    constexpr int T = 2 * NQ, D = Product::D;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int t = blockIdx.x;
+    const int64_t tile = (int64_t)c.expert * (hidden >> 6) + t, row = tile * 64 + lane;
+    auto pair_of = [&](int j) { return (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8); };
+    const int workers = kDefaultWaves * gridDim.z, worker = blockIdx.z * kDefaultWaves + w;
+    PairRow entries;
+    entries.load(down.lut + row * 16, w);
+    const int32_t *rp = down.nnz ? down.row_ptr + row : (const int32_t *)dev::g_placeholder;
+    const int lo = rp[0], hi = rp[1];
+    const int halves = inter >> 7, n = max(0, (halves - worker + workers - 1) / workers); // of this wave
+    const uint16_t *xr[NQ];
+#pragma unroll
+    for (int h = 0; h < NQ; ++h) {
+        const int j = 4 * h + (lane & 3);
+        xr[h] = (j < T ? a.hi : a.lo) + pair_of(min(j & (T - 1), c.count - 1)) * inter;
+    }
+    Product p;
+    auto load = [&](int k, int i) {
+        p.load(k, down.packed + tile * halves * (4 * 1024), xr, i < n ? worker + i * workers : -1);
+    };
+#pragma unroll
+    for (int k = 0; k < D; ++k) load(k, k);
+    entries.store(space, w);
+    dev::lds_barrier();
+    p.clear();
+    for (int i = 0; i < n; i += D) {
+#pragma unroll
+        for (int k = 0; k < D; ++k) {
+            p.multiply(k, space);
+            load(k, i + k + D);
+        }
+    }
+    float sum[4 * NQ];
+    p.sums(sum);
+    __syncthreads(); // the table is done with
+    if (down.nnz > 0) {
+        auto whole_of = [&](int j) { return a.whole + pair_of(j) * inter; };
+        const bool staged = c.count * inter * 4 <= room;
+        if (staged) {
+            stage_rows(c.count, inter * 4, [&](int j) { return (const uint8_t *)whole_of(j); }, space);
+            all_loads_done();
+        }
+        Outliers out;
+        out.set(down, lo, hi, worker, workers);
+        const float *xs = (const float *)space;
+        if (staged)
+            out.add<T>(c.count, [&](int j, int col) { return xs[j * inter + col]; }, sum);
+        else
+            out.add<T>(c.count, [&](int j, int col) { return whole_of(j)[col]; }, sum);
+        __syncthreads(); // the space is used again below
+    }
+    float *const red = (float *)space;
+#pragma unroll
+    for (int j = 0; j < T; ++j) red[(w * T + j) * 64 + lane] = sum[j] + sum[T + j] * 0x1p-11f;
+    __syncthreads();
+    for (int j = w; j < c.count; j += kDefaultWaves) {
+        float v = 0.f;
+        for (int k = 0; k < kDefaultWaves; ++k) v += red[(k * T + j) * 64 + lane];
+        partial[(blockIdx.z * pairs + pair_of(j)) * hidden + t * 64 + lane] = v;
+    }
+}
+
+template <int MAXQ>
+__global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down_table(Projection down, Activations a,
+                                                                     const int32_t *ids, int batch, int experts, int topk,
+                                                                     int hidden, int inter, int room, float *partial)
+{
+    __shared__ ChosenLds chosen[kDefaultWaves];
+    extern __shared__ __align__(16) uint8_t space[];
+    ChosenLds &lds = chosen[threadIdx.x >> 6];
+    const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
+    if (c.expert < 0) return;
+    const int64_t pairs = batch * topk;
+    if (MAXQ >= 4 && c.count > 8)
+        down_table_body<MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+    else if (MAXQ >= 2 && c.count > 4)
+        down_table_body<MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+    else if (c.count > 2)
+        down_table_body<2>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+    else
+        down_table_body<1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+}
+
 template <int BITS, int NQ>
 __device__ __forceinline__ void down_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
                                           int topk, int hidden, int inter, int parts, int room, int64_t pairs,
@@ -1022,6 +1327,9 @@ Projection projection(const sqllm_experts &p)
 // 16 tokens, 128 experts 4096x1536: 146, 147 and 150).
 constexpr int64_t kStageRoom = 64 << 10;
 
+bool gate_by_table(int bits, int cols) { return bits == 4 && cols >= 2048; }
+bool down_by_table(int bits, int cols) { return bits == 4 && cols >= 3584; }
+
 template <int BITS, int MAXQ>
 sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weights, const Projection &gate,
                       const Projection &up, const Projection &down, int batch, int experts, int topk, int hidden,
@@ -1039,16 +1347,41 @@ sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weight
     auto space = [&](int64_t stage) { return std::max(red, (size_t)std::min(stage, kStageRoom)); };
     const size_t gate_lds = space(gate.nnz + up.nnz > 0 ? (int64_t)batch * hidden * 2 : 0);
     const size_t down_lds = space(down.nnz > 0 ? (int64_t)batch * inter * 4 : 0);
-    static std::atomic<uint64_t> gate_asked{0}, down_asked{0};
-    dev::raise_lds_limit((const void *)experts_gate_up<BITS, MAXQ>, gate_asked, (int)kStageRoom);
-    dev::raise_lds_limit((const void *)experts_down<BITS, MAXQ>, down_asked, (int)kStageRoom);
     const int down_parts = down_parts_for((int64_t)used * (hidden / 64) * splits, inter / splits);
     const int down_wgs = (hidden / 64 * down_parts + kDefaultWaves - 1) / kDefaultWaves;
-    hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(inter / 64, used), dim3(64 * kDefaultWaves),
-                       gate_lds, stream, gate, up, x, ids, batch, experts, topk, hidden, inter, (int)gate_lds, a);
-    hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(down_wgs, used, splits),
-                       dim3(64 * kDefaultWaves), down_lds, stream, down, a, ids, batch, experts, topk, hidden, inter,
-                       down_parts, (int)down_lds, part);
+    const dim3 threads(64 * kDefaultWaves);
+    bool by_table = false;
+    if constexpr (BITS == 4) {
+        if ((by_table = gate_by_table(BITS, hidden))) {
+            const int lds = (int)std::max((size_t)kPairTable, gate_lds);
+            static std::atomic<uint64_t> asked{0};
+            dev::raise_lds_limit((const void *)experts_gate_up_table<MAXQ>, asked, (int)kStageRoom);
+            hipLaunchKernelGGL((experts_gate_up_table<MAXQ>), dim3(inter / 64, used), threads, lds, stream, gate, up, x,
+                               ids, batch, experts, topk, hidden, inter, lds, a);
+        }
+    }
+    if (!by_table) {
+        static std::atomic<uint64_t> asked{0};
+        dev::raise_lds_limit((const void *)experts_gate_up<BITS, MAXQ>, asked, (int)kStageRoom);
+        hipLaunchKernelGGL((experts_gate_up<BITS, MAXQ>), dim3(inter / 64, used), threads, gate_lds, stream, gate, up, x, ids,
+                           batch, experts, topk, hidden, inter, (int)gate_lds, a);
+    }
+    by_table = false;
+    if constexpr (BITS == 4) {
+        if ((by_table = down_by_table(BITS, inter / splits))) {
+            const int lds = (int)std::max((size_t)kPairTable, down_lds);
+            static std::atomic<uint64_t> asked{0};
+            dev::raise_lds_limit((const void *)experts_down_table<MAXQ>, asked, (int)kStageRoom);
+            hipLaunchKernelGGL((experts_down_table<MAXQ>), dim3(hidden / 64, used, splits), threads, lds, stream, down, a,
+                               ids, batch, experts, topk, hidden, inter, lds, part);
+        }
+    }
+    if (!by_table) {
+        static std::atomic<uint64_t> asked{0};
+        dev::raise_lds_limit((const void *)experts_down<BITS, MAXQ>, asked, (int)kStageRoom);
+        hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(down_wgs, used, splits), threads, down_lds, stream, down, a, ids,
+                           batch, experts, topk, hidden, inter, down_parts, (int)down_lds, part);
+    }
     hipLaunchKernelGGL(experts_combine, dim3(hidden / 256, batch), dim3(256), 0, stream, part, ids, weights, batch,
                        experts, topk, hidden, splits, y);
     return launched();

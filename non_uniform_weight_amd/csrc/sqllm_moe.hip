@@ -254,12 +254,12 @@ __global__ void __launch_bounds__(64) route_choose(const double *__restrict__ lo
 // of one expert in use and all the tokens that chose it; its waves share the
 // columns in half groups of 128 and add up their fp32 sums in LDS.
 //
-// Decoding without tables in memory: a row's centroids stay in registers as
-// bytes, the low bytes of the fp16 values in one set and the high bytes in
-// another, and v_perm_b32 picks four of them at once by four codes.  The
-// products of a model's experts are short (a tile of 768 to 4096 columns), so
-// the lookup tables in LDS that the long products of sqllm_device.h build per
-// tile would cost as much as they save here.
+// Two decodes.  Without a table in memory: a row's centroids stay in registers
+// as bytes, the low bytes of the fp16 values in one set and the high bytes in
+// another, and v_perm_b32 picks four of them at once by four codes.  Or with a
+// table of pairs of centroids in LDS (below), which a workgroup has to write
+// first; it pays where a tile has many columns, and the more the wider the
+// codes (gate_by_table and down_by_table).
 //
 // Products: v_mfma_f32_4x4x4f16 with CBSZ = 4 multiplies each lane's own four
 // weights (B: lane = row) by the four activations of four tokens that block
@@ -670,49 +670,54 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
         for (int r = 0; r < 4; ++r) sum[4 * h + r] = C == 2 ? acc[h][0][r] + acc[h][C - 1][r] : acc[h][0][r];
 }
 
-// The other decode, at 4 bits: a table in LDS of the tile's pairs of centroids,
-// entry [second code][first code][row] of two fp16 values (64 KB; a row's
-// entries share a bank of its own).  A pair of codes is a byte, and the address
-// of its entry that byte above the row's: one v_perm_b32 and one LDS read for
-// two weights, in the order of their columns, where the decode from registers
-// takes six vector instructions.
-constexpr int kPairTable = 256 * 64 * 4;
+// The other decode, at 3 and 4 bits: a table in LDS of the tile's pairs of
+// centroids, entry [second code][first code][row] of two fp16 values (16 or 64
+// KB; a row's entries share a bank of its own).  A pair of codes is a byte, and
+// the address of its entry that byte above the row's: one v_perm_b32 and one LDS
+// read for two weights, in the order of their columns, where the decode from
+// registers takes six vector instructions at 4 bits and three at 3.
+template <int BITS>
+constexpr int kPairTable = (1 << 2 * BITS) * 64 * 4;
+template <int BITS>
+constexpr int kBuilders = 1 << (BITS - 1); // waves that write a table, two second codes each
 
 // A row's centroids, and those of the two second codes whose entries this wave
 // writes.
+template <int BITS>
 struct PairRow {
-    uint32_t first[8], second;
+    uint32_t first[1 << (BITS - 1)], second;
 
-    __device__ __forceinline__ void load(const uint16_t *row, int wave)
+    __device__ __forceinline__ void load(const uint16_t *row, int builder)
     {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < (1 << BITS) / 8; ++q) {
             const u32x4 v = ((const u32x4 *)row)[q];
             first[4 * q] = v.x, first[4 * q + 1] = v.y, first[4 * q + 2] = v.z, first[4 * q + 3] = v.w;
         }
-        second = ((const uint32_t *)row)[wave];
+        second = ((const uint32_t *)row)[builder];
     }
 
-    __device__ __forceinline__ void store(uint8_t *table, int wave) const
+    __device__ __forceinline__ void store(uint8_t *table, int builder) const
     {
-        static_assert(kDefaultWaves == 8, "two of the sixteen second codes a wave");
-        uint32_t *to = (uint32_t *)table + wave * (2 * 16 * 64) + (threadIdx.x & 63);
+        uint32_t *to = (uint32_t *)table + (builder << (BITS + 7)) + (threadIdx.x & 63);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-                to[(s * 16 + c) * 64] =
+            for (int c = 0; c < 1 << BITS; ++c)
+                to[((s << BITS) + c) * 64] =
                     perm(second, first[c / 2], (c & 1 ? 0x0302 : 0x0100) | (s ? 0x07060000 : 0x05040000));
     }
 };
 
-// A ring of a wave's half groups on their way, D of them: codes and
-// activations; and the sums of one matrix.
-template <int NQ>
+// The half group that a wave has on its way, codes and activations, and the
+// sums of one matrix.  (One is enough with sixteen waves a compute unit: with
+// two or three the registers do not hold the table's answers too, 4 tokens, 8
+// experts 4096x14336 at 4 bits 132 and 152 us a call against 114.)
+template <int BITS, int NQ>
 struct TableProduct {
-    static constexpr int D = NQ == 4 ? 1 : 2, C = NQ == 1 ? 2 : 1;
-    Half<4> codes[D];
-    u32x4 x[D][NQ];
+    static constexpr int C = NQ == 1 ? 2 : 1; // accumulator chains, as in tile_product
+    Half<BITS> codes;
+    u32x4 x[NQ];
     f32x4 acc[NQ][C];
 
     __device__ __forceinline__ void clear()
@@ -723,37 +728,36 @@ struct TableProduct {
             for (int c = 0; c < C; ++c) acc[h][c] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    // Half group g (128 columns) of a tile into slot k; g < 0: zeros, so that
-    // every step issues the same loads.
-    __device__ __forceinline__ void load(int k, const uint8_t *tile, const uint16_t *const (&rows)[NQ], int g)
+    // Half group g (128 columns) of a tile.
+    __device__ __forceinline__ void load(const uint8_t *tile, const uint16_t *const (&rows)[NQ], int g)
     {
         const int lane = threadIdx.x & 63;
-        codes[k].load((g >= 0 ? tile + (int64_t)g * (4 * 1024) : (const uint8_t *)dev::g_placeholder) + lane * 16);
+        codes.load(tile + (int64_t)g * (BITS * 1024) + lane * 16);
 #pragma unroll
-        for (int h = 0; h < NQ; ++h)
-            x[k][h] = *(const u32x4 *)((g >= 0 ? rows[h] + 128 * g : (const uint16_t *)dev::g_placeholder) + 8 * (lane >> 2));
+        for (int h = 0; h < NQ; ++h) x[h] = *(const u32x4 *)(rows[h] + 128 * g + 8 * (lane >> 2));
     }
 
-    __device__ __forceinline__ void multiply(int k, const uint8_t *table)
+    __device__ __forceinline__ void multiply(const uint8_t *table)
     {
         const uint32_t row = (threadIdx.x & 63) * 4; // of an entry, below the pair's byte
         [&]<int... Ns>(std::integer_sequence<int, Ns...>) {
             (
                 [&] {
-                    const uint32_t v = codes[k].template pairs<Ns>();
+                    uint32_t v = codes.template pairs<Ns>();
+                    if constexpr (BITS == 3) v &= 0x3F3F3F3F;
                     const uint32_t e0 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0400));
                     const uint32_t e1 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0500));
                     const uint32_t e2 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0600));
                     const uint32_t e3 = *(const uint32_t *)(table + perm(v, row, 0x0C0C0700));
 #pragma unroll
                     for (int h = 0; h < NQ; ++h)
-                        acc[h][0] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2{x[k][h].x, x[k][h].y}),
+                        acc[h][0] = __builtin_amdgcn_mfma_f32_4x4x4f16(__builtin_bit_cast(half4_t, u32x2{x[h].x, x[h].y}),
                                                                       __builtin_bit_cast(half4_t, u32x2{e0, e1}), acc[h][0], 4,
                                                                       Ns, 0);
 #pragma unroll
                     for (int h = 0; h < NQ; ++h)
                         acc[h][C - 1] = __builtin_amdgcn_mfma_f32_4x4x4f16(
-                            __builtin_bit_cast(half4_t, u32x2{x[k][h].z, x[k][h].w}),
+                            __builtin_bit_cast(half4_t, u32x2{x[h].z, x[h].w}),
                             __builtin_bit_cast(half4_t, u32x2{e2, e3}), acc[h][C - 1], 4, Ns, 0);
                 }(),
                 ...);
@@ -863,59 +867,52 @@ __device__ __forceinline__ void gate_up_body(const Projection &gate, const Proje
     }
 }
 
-// The same by pair tables: all waves have the gate's tile, then the up's, each
-// at every eighth half group, in one stream of loads; the up's table takes the
-// gate's place, so that two workgroups share a compute unit.
+// The same at 4 bits by pair tables: all waves have the gate's tile, then the
+// up's, each at every eighth half group, in one stream of loads.  The up's
+// table takes the gate's place, so that two workgroups share a compute unit.
 template <int NQ>
 __device__ __forceinline__ void gate_up_table_body(const Projection &gate, const Projection &up, const uint16_t *x,
                                                    const ChosenLds &lds, Chosen c, int topk, int hidden, int inter,
                                                    int room, Activations a, uint8_t *space)
 {
-    using Product = TableProduct<NQ>;
-    constexpr int D = Product::D;
+    constexpr int BITS = 4;
+    static_assert(kBuilders<BITS> == kDefaultWaves);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x;
     const int64_t tile = (int64_t)c.expert * (inter >> 6) + t, row = tile * 64 + lane;
     auto row_of = [&](int j) { return x + (int64_t)(lds.list[j] & 255) * hidden; };
-    PairRow first, second;
-    first.load(gate.lut + row * 16, w);
-    second.load(up.lut + row * 16, w);
+    PairRow<BITS> entries, next;
+    entries.load(gate.lut + (row << BITS), w);
+    next.load(up.lut + (row << BITS), w);
     const int32_t *grp = gate.nnz ? gate.row_ptr + row : (const int32_t *)dev::g_placeholder;
     const int32_t *urp = up.nnz ? up.row_ptr + row : (const int32_t *)dev::g_placeholder;
     const int g_lo = grp[0], g_hi = grp[1], u_lo = urp[0], u_hi = urp[1];
     const int halves = hidden >> 7, n = max(0, (halves - w + kDefaultWaves - 1) / kDefaultWaves); // of this wave
-    const int steps = (n + D - 1) / D * D;
-    const int64_t from = tile * halves * (4 * 1024);
+    const int64_t from = tile * halves * (BITS * 1024);
     const uint16_t *xr[NQ];
 #pragma unroll
     for (int h = 0; h < NQ; ++h) xr[h] = row_of(min(4 * h + (lane & 3), c.count - 1)); // past the last: a copy, dropped
-    Product p;
-    auto load = [&](int k, int i) { // gate's steps, then up's
-        const int at = i < steps ? i : i - steps;
-        p.load(k, (i < steps ? gate : up).packed + from, xr, at < n ? w + at * kDefaultWaves : -1);
+    TableProduct<BITS, NQ> p;
+    auto load = [&](int i) { // gate's n, then up's
+        if (i < 2 * n) p.load((i < n ? gate : up).packed + from, xr, w + (i < n ? i : i - n) * kDefaultWaves);
     };
-    auto run = [&](int first) {
+    auto run = [&](int first, float (&to)[4 * NQ]) {
         p.clear();
-        for (int i = first; i < first + steps; i += D) {
-#pragma unroll
-            for (int k = 0; k < D; ++k) {
-                p.multiply(k, space);
-                load(k, i + k + D);
-            }
+        for (int i = first; i < first + n; ++i) {
+            p.multiply(space);
+            load(i + 1);
         }
+        p.sums(to);
     };
     float sum[2][4 * NQ];
-#pragma unroll
-    for (int k = 0; k < D; ++k) load(k, k);
-    first.store(space, w);
+    load(0);
+    entries.store(space, w);
     dev::lds_barrier();
-    run(0);
-    p.sums(sum[0]);
+    run(0, sum[0]);
     dev::lds_barrier(); // the gate's table is done with
-    second.store(space, w);
+    next.store(space, w);
     dev::lds_barrier();
-    run(steps);
-    p.sums(sum[1]);
+    run(n, sum[1]);
     __syncthreads(); // the up's too
     if (gate.nnz + up.nnz > 0) {
         const bool staged = c.count * hidden * 2 <= room;
@@ -997,20 +994,20 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Project
 // share a tile and split.
 // Grid (ceil(hidden / 64 / (8 / parts)), experts in use at most, splits).
 // ---------------------------------------------------------------------------
-template <int NQ>
+// The same by pair tables: a tile to a workgroup.
+template <int BITS, int NQ>
 __device__ __forceinline__ void down_table_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
                                                 int topk, int hidden, int inter, int room, int64_t pairs,
                                                 float *partial, uint8_t *space)
 {
-    using Product = TableProduct<NQ>;
-    constexpr int T = 2 * NQ, D = Product::D;
+    constexpr int T = 2 * NQ;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.x;
     const int64_t tile = (int64_t)c.expert * (hidden >> 6) + t, row = tile * 64 + lane;
     auto pair_of = [&](int j) { return (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8); };
     const int workers = kDefaultWaves * gridDim.z, worker = blockIdx.z * kDefaultWaves + w;
-    PairRow entries;
-    entries.load(down.lut + row * 16, w);
+    PairRow<BITS> entries;
+    entries.load(down.lut + (row << BITS), w % kBuilders<BITS>);
     const int32_t *rp = down.nnz ? down.row_ptr + row : (const int32_t *)dev::g_placeholder;
     const int lo = rp[0], hi = rp[1];
     const int halves = inter >> 7, n = max(0, (halves - worker + workers - 1) / workers); // of this wave
@@ -1020,26 +1017,22 @@ __device__ __forceinline__ void down_table_body(const Projection &down, Activati
         const int j = 4 * h + (lane & 3);
         xr[h] = (j < T ? a.hi : a.lo) + pair_of(min(j & (T - 1), c.count - 1)) * inter;
     }
-    Product p;
-    auto load = [&](int k, int i) {
-        p.load(k, down.packed + tile * halves * (4 * 1024), xr, i < n ? worker + i * workers : -1);
+    TableProduct<BITS, NQ> p;
+    auto load = [&](int i) {
+        if (i < n) p.load(down.packed + tile * halves * (BITS * 1024), xr, worker + i * workers);
     };
-#pragma unroll
-    for (int k = 0; k < D; ++k) load(k, k);
-    entries.store(space, w);
+    load(0);
+    if (w < kBuilders<BITS>) entries.store(space, w);
     dev::lds_barrier();
     p.clear();
-    for (int i = 0; i < n; i += D) {
-#pragma unroll
-        for (int k = 0; k < D; ++k) {
-            p.multiply(k, space);
-            load(k, i + k + D);
-        }
+    for (int i = 0; i < n; ++i) {
+        p.multiply(space);
+        load(i + 1);
     }
     float sum[4 * NQ];
     p.sums(sum);
     __syncthreads(); // the table is done with
-    if (down.nnz > 0) {
+    if (down.nnz > 0) { // (staged now, the table had the space)
         auto whole_of = [&](int j) { return a.whole + pair_of(j) * inter; };
         const bool staged = c.count * inter * 4 <= room;
         if (staged) {
@@ -1066,7 +1059,7 @@ __device__ __forceinline__ void down_table_body(const Projection &down, Activati
     }
 }
 
-template <int MAXQ>
+template <int BITS, int MAXQ>
 __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down_table(Projection down, Activations a,
                                                                      const int32_t *ids, int batch, int experts, int topk,
                                                                      int hidden, int inter, int room, float *partial)
@@ -1078,13 +1071,13 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down_table(Proj
     if (c.expert < 0) return;
     const int64_t pairs = batch * topk;
     if (MAXQ >= 4 && c.count > 8)
-        down_table_body<MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+        down_table_body<BITS, MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
     else if (MAXQ >= 2 && c.count > 4)
-        down_table_body<MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+        down_table_body<BITS, MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
     else if (c.count > 2)
-        down_table_body<2>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+        down_table_body<BITS, 2>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
     else
-        down_table_body<1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
+        down_table_body<BITS, 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
 }
 
 template <int BITS, int NQ>
@@ -1327,8 +1320,20 @@ Projection projection(const sqllm_experts &p)
 // 16 tokens, 128 experts 4096x1536: 146, 147 and 150).
 constexpr int64_t kStageRoom = 64 << 10;
 
-bool gate_by_table(int bits, int cols) { return bits == 4 && cols >= 2048; }
-bool down_by_table(int bits, int cols) { return bits == 4 && cols >= 3584; }
+// Which decode the products take: pair tables for gate and up at 4 bits from
+// 1024 columns on (us of a call with registers and with tables: 8 tokens, 128
+// experts 2048x768 52 and 44, 64 experts 1024x2048 41.4 and 40.5, 512x2048 28.6
+// and 29.0; one token, 2 of 8 experts 4096x11008 60 and 47; at 3 bits 42 and
+// 42, 16 tokens, 128 experts 4096x1536 161 and 162, one token 4096x2048 23 and
+// 26) ...
+bool gate_by_table(int hidden) { return hidden >= 1024; }
+
+// ... and for down at 3 and 4 bits where eight waves share a tile anyway or
+// have 2048 columns (one token, 6 of 64 experts 2048x1280 at 3 bits 20.1 and
+// 18.7, 4 of 64 1024x2048 34 and 31 with 8 tokens, 8 of 8 4096x14336 108 and
+// 101, at 4 bits 141 and 116; but 128 experts 4096x1536 161 and 172, 2048x768
+// 36 and 39, at 4 bits 190 and 192, 44 and 46).
+bool down_by_table(int parts, int cols) { return parts == kDefaultWaves || cols >= 2048; }
 
 template <int BITS, int MAXQ>
 sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weights, const Projection &gate,
@@ -1352,8 +1357,8 @@ sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weight
     const dim3 threads(64 * kDefaultWaves);
     bool by_table = false;
     if constexpr (BITS == 4) {
-        if ((by_table = gate_by_table(BITS, hidden))) {
-            const int lds = (int)std::max((size_t)kPairTable, gate_lds);
+        if ((by_table = gate_by_table(hidden))) {
+            const int lds = (int)std::max((size_t)kPairTable<BITS>, gate_lds);
             static std::atomic<uint64_t> asked{0};
             dev::raise_lds_limit((const void *)experts_gate_up_table<MAXQ>, asked, (int)kStageRoom);
             hipLaunchKernelGGL((experts_gate_up_table<MAXQ>), dim3(inter / 64, used), threads, lds, stream, gate, up, x,
@@ -1367,12 +1372,12 @@ sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weight
                            batch, experts, topk, hidden, inter, (int)gate_lds, a);
     }
     by_table = false;
-    if constexpr (BITS == 4) {
-        if ((by_table = down_by_table(BITS, inter / splits))) {
-            const int lds = (int)std::max((size_t)kPairTable, down_lds);
+    if constexpr (BITS > 2) {
+        if ((by_table = down_by_table(down_parts, inter / splits))) {
+            const int lds = (int)std::max((size_t)kPairTable<BITS>, down_lds);
             static std::atomic<uint64_t> asked{0};
-            dev::raise_lds_limit((const void *)experts_down_table<MAXQ>, asked, (int)kStageRoom);
-            hipLaunchKernelGGL((experts_down_table<MAXQ>), dim3(hidden / 64, used, splits), threads, lds, stream, down, a,
+            dev::raise_lds_limit((const void *)experts_down_table<BITS, MAXQ>, asked, (int)kStageRoom);
+            hipLaunchKernelGGL((experts_down_table<BITS, MAXQ>), dim3(hidden / 64, used, splits), threads, lds, stream, down, a,
                                ids, batch, experts, topk, hidden, inter, lds, part);
         }
     }

@@ -22,6 +22,8 @@ namespace {
 
 constexpr int kMaxExperts = SQLLM_MOE_MAX_EXPERTS;
 constexpr int kMaxTopk = SQLLM_MOE_MAX_TOPK;
+constexpr int kLogWaves = 3;
+static_assert(kDefaultWaves == 1 << kLogWaves);
 constexpr int64_t kMaxWidth = 65536; // hidden, inter: 16-bit columns of the outliers
 
 // ---------------------------------------------------------------------------
@@ -505,16 +507,16 @@ struct Outliers {
     const uint16_t *cols, *vals; // the tile's
     int lo, count;               // this lane's row: entries [lo, lo + count)
     int len;                     // the tile's
-    int share, shares;
+    int share, shares, log; // log2 of shares
     int64_t left;                // entries from the tile's first to the arrays' end
 
-    __device__ __forceinline__ void set(const Projection &p, int rp_lo, int rp_hi, int worker, int workers)
+    __device__ __forceinline__ void set(const Projection &p, int rp_lo, int rp_hi, int worker, int log_workers)
     {
         const int nz0 = __builtin_amdgcn_readfirstlane(rp_lo); // all else relative to the tile's first
         lo = rp_lo - nz0, count = rp_hi - rp_lo;
         len = __builtin_amdgcn_readlane(rp_hi, 63) - nz0;
         cols = p.col + nz0, vals = p.val + nz0;
-        share = worker, shares = workers;
+        share = worker, shares = 1 << log_workers, log = log_workers;
         left = p.nnz - nz0;
     }
 
@@ -522,8 +524,8 @@ struct Outliers {
     template <int T, int N, typename V>
     __device__ __forceinline__ void add(int tokens, V value, float (&sum)[N]) const
     {
-        const int steps = ((int)wave_max((uint32_t)count) + 4 * shares - 1) / (4 * shares);
-        const int chunks = (len + 64 * shares - 1) / (64 * shares);
+        const int steps = ((int)wave_max((uint32_t)count) + 4 * shares - 1) >> (log + 2);
+        const int chunks = (len + 64 * shares - 1) >> (log + 6);
         if (left >= 4 && steps <= 2 * chunks)
             by_rows<T>(tokens, value, sum, steps);
         else
@@ -564,7 +566,7 @@ struct Outliers {
     template <int T, int N, typename V>
     __device__ __forceinline__ void by_chunks(int tokens, V value, float (&sum)[N]) const
     {
-        const int lane = threadIdx.x & 63, per = len / shares, extra = len - per * shares;
+        const int lane = threadIdx.x & 63, per = len >> log, extra = len - per * shares;
         const int v0 = share * per + min(share, extra), v1 = v0 + per + (share < extra ? 1 : 0);
         constexpr int kAtOnce = 2;
         for (int base = v0; base < v1; base += 64 * kAtOnce) {
@@ -591,11 +593,12 @@ struct Outliers {
     }
 };
 
-// This wave's share (worker `worker` of `workers`) of one matrix for one tile:
-// every workers-th half group; its share of the outliers is left in `out`.  x(j) is the fp16 row of matrix column j.
+// This wave's share (worker `worker` of 2^log_workers) of one matrix for one
+// tile: every so many half groups; its share of the outliers is left in `out`.
+// x(j) is the fp16 row of matrix column j.
 // Column 4h + i of the matrix steps ends in sum[4h + i].
 template <int BITS, int NQ, typename X>
-__device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int groups, int worker, int workers, X x,
+__device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int groups, int worker, int log_workers, X x,
                                              float (&sum)[4 * NQ], Outliers &out)
 {
     // half groups in flight, as many as fit 128 registers without spilling
@@ -607,7 +610,8 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
     table.load(p.lut + (row << BITS));
     const int32_t *rp = p.nnz ? p.row_ptr + row : (const int32_t *)dev::g_placeholder;
     const int rp_lo = rp[0], rp_hi = rp[1];
-    const int n = max(0, (2 * groups - worker + workers - 1) / workers); // half groups of this wave
+    const int workers = 1 << log_workers;
+    const int n = (2 * groups - worker + workers - 1) >> log_workers; // half groups of this wave
     const uint8_t *codes = p.packed + tile * groups * (2 * BITS * 1024);
     const uint16_t *xr[NQ];
 #pragma unroll
@@ -652,7 +656,7 @@ __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, 
     };
 #pragma unroll
     for (int k = 0; k < D; ++k) load(k, k);
-    out.set(p, rp_lo, rp_hi, worker, workers);
+    out.set(p, rp_lo, rp_hi, worker, log_workers);
     int i = 0;
     for (; i + D <= n; i += D) {
 #pragma unroll
@@ -841,7 +845,7 @@ __device__ __forceinline__ void gate_up_body(const Projection &gate, const Proje
         stage_rows(c.count, hidden * 2, [&](int j) { return (const uint8_t *)row_of(j); }, space);
     float sum[4 * NQ];
     Outliers out;
-    tile_product<BITS, NQ>(w & 1 ? up : gate, tile, hidden >> 8, w >> 1, kDefaultWaves / 2,
+    tile_product<BITS, NQ>(w & 1 ? up : gate, tile, hidden >> 8, w >> 1, kLogWaves - 1,
                            [&](int j) { return row_of(min(j, c.count - 1)); }, // past the last: a copy, dropped
                            sum, out);
     if (staged) {
@@ -887,7 +891,7 @@ __device__ __forceinline__ void gate_up_table_body(const Projection &gate, const
     const int32_t *grp = gate.nnz ? gate.row_ptr + row : (const int32_t *)dev::g_placeholder;
     const int32_t *urp = up.nnz ? up.row_ptr + row : (const int32_t *)dev::g_placeholder;
     const int g_lo = grp[0], g_hi = grp[1], u_lo = urp[0], u_hi = urp[1];
-    const int halves = hidden >> 7, n = max(0, (halves - w + kDefaultWaves - 1) / kDefaultWaves); // of this wave
+    const int halves = hidden >> 7, n = (halves - w + kDefaultWaves - 1) >> kLogWaves; // of this wave
     const int64_t from = tile * halves * (BITS * 1024);
     const uint16_t *xr[NQ];
 #pragma unroll
@@ -926,7 +930,7 @@ __device__ __forceinline__ void gate_up_table_body(const Projection &gate, const
             const Projection &q = s ? up : gate;
             if (q.nnz == 0) continue;
             Outliers out;
-            out.set(q, s ? u_lo : g_lo, s ? u_hi : g_hi, w, kDefaultWaves);
+            out.set(q, s ? u_lo : g_lo, s ? u_hi : g_hi, w, kLogWaves);
             if (staged)
                 out.add<4 * NQ>(c.count, [&](int j, int col) { return dev::f16_to_f32(xs[j * hidden + col]); }, sum[s]);
             else
@@ -1005,17 +1009,19 @@ __device__ __forceinline__ void down_table_body(const Projection &down, Activati
     const int t = blockIdx.x;
     const int64_t tile = (int64_t)c.expert * (hidden >> 6) + t, row = tile * 64 + lane;
     auto pair_of = [&](int j) { return (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8); };
-    const int workers = kDefaultWaves * gridDim.z, worker = blockIdx.z * kDefaultWaves + w;
+    const int log_workers = kLogWaves + __builtin_ctz(gridDim.z), workers = 1 << log_workers; // splits: a power of two
+    const int worker = blockIdx.z * kDefaultWaves + w;
+    const int64_t lo_from_hi = a.lo - a.hi; // (a choice between the pointers puts them in scratch memory)
     PairRow<BITS> entries;
     entries.load(down.lut + (row << BITS), w % kBuilders<BITS>);
     const int32_t *rp = down.nnz ? down.row_ptr + row : (const int32_t *)dev::g_placeholder;
     const int lo = rp[0], hi = rp[1];
-    const int halves = inter >> 7, n = max(0, (halves - worker + workers - 1) / workers); // of this wave
+    const int halves = inter >> 7, n = (halves - worker + workers - 1) >> log_workers; // of this wave
     const uint16_t *xr[NQ];
 #pragma unroll
     for (int h = 0; h < NQ; ++h) {
         const int j = 4 * h + (lane & 3);
-        xr[h] = (j < T ? a.hi : a.lo) + pair_of(min(j & (T - 1), c.count - 1)) * inter;
+        xr[h] = a.hi + (j < T ? 0 : lo_from_hi) + pair_of(min(j & (T - 1), c.count - 1)) * inter;
     }
     TableProduct<BITS, NQ> p;
     auto load = [&](int i) {
@@ -1040,7 +1046,7 @@ __device__ __forceinline__ void down_table_body(const Projection &down, Activati
             all_loads_done();
         }
         Outliers out;
-        out.set(down, lo, hi, worker, workers);
+        out.set(down, lo, hi, worker, log_workers);
         const float *xs = (const float *)space;
         if (staged)
             out.add<T>(c.count, [&](int j, int col) { return xs[j * inter + col]; }, sum);
@@ -1082,24 +1088,26 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down_table(Proj
 
 template <int BITS, int NQ>
 __device__ __forceinline__ void down_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
-                                          int topk, int hidden, int inter, int parts, int room, int64_t pairs,
+                                          int topk, int hidden, int inter, int log_parts, int room, int64_t pairs,
                                           float *partial, uint8_t *space)
 {
     constexpr int T = 2 * NQ; // tokens
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int tiles = hidden >> 6, part = w & (parts - 1), t = blockIdx.x * (kDefaultWaves / parts) + w / parts;
+    const int parts = 1 << log_parts, tiles = hidden >> 6, part = w & (parts - 1);
+    const int t = (blockIdx.x << (kLogWaves - log_parts)) + (w >> log_parts);
     const bool owns = t < tiles; // the last workgroup may have waves too many
     const int64_t tile = (int64_t)c.expert * tiles + min(t, tiles - 1);
     auto pair_of = [&](int j) { return (int64_t)(lds.list[j] & 255) * topk + (lds.list[j] >> 8); };
     float *const to = partial + blockIdx.z * pairs * hidden + t * 64 + lane;
     float sum[4 * NQ];
-    const int workers = parts * gridDim.z, worker = blockIdx.z * parts + part;
+    const int log_workers = log_parts + __builtin_ctz(gridDim.z), worker = blockIdx.z * parts + part;
+    const int64_t lo_from_hi = a.lo - a.hi; // (a choice between the pointers puts them in scratch memory)
     auto whole_of = [&](int j) { return a.whole + pair_of(j) * inter; };
     const bool staged = c.count * inter * 4 <= room && down.nnz > 0;
     if (staged) stage_rows(c.count, inter * 4, [&](int j) { return (const uint8_t *)whole_of(j); }, space);
     Outliers out;
-    tile_product<BITS, NQ>(down, tile, inter >> 8, worker, workers,
-                           [&](int j) { return (j < T ? a.hi : a.lo) + pair_of(min(j & (T - 1), c.count - 1)) * inter; },
+    tile_product<BITS, NQ>(down, tile, inter >> 8, worker, log_workers,
+                           [&](int j) { return a.hi + (j < T ? 0 : lo_from_hi) + pair_of(min(j & (T - 1), c.count - 1)) * inter; },
                            sum, out);
     if (staged) {
         all_loads_done();
@@ -1131,7 +1139,7 @@ __device__ __forceinline__ void down_body(const Projection &down, Activations a,
 template <int BITS, int MAXQ>
 __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down(Projection down, Activations a,
                                                                       const int32_t *ids, int batch, int experts,
-                                                                      int topk, int hidden, int inter, int parts,
+                                                                      int topk, int hidden, int inter, int log_parts,
                                                                       int room, float *partial)
 {
     __shared__ ChosenLds chosen[kDefaultWaves];
@@ -1141,13 +1149,13 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down(Projection
     if (c.expert < 0) return;
     const int64_t pairs = batch * topk;
     if (MAXQ >= 4 && c.count > 8)
-        down_body<BITS, MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
+        down_body<BITS, MAXQ >= 4 ? 8 : 1>(down, a, lds, c, topk, hidden, inter, log_parts, room, pairs, partial, space);
     else if (MAXQ >= 2 && c.count > 4)
-        down_body<BITS, MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
+        down_body<BITS, MAXQ >= 2 ? 4 : 1>(down, a, lds, c, topk, hidden, inter, log_parts, room, pairs, partial, space);
     else if (MAXQ >= 1 && c.count > 2)
-        down_body<BITS, MAXQ >= 1 ? 2 : 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
+        down_body<BITS, MAXQ >= 1 ? 2 : 1>(down, a, lds, c, topk, hidden, inter, log_parts, room, pairs, partial, space);
     else
-        down_body<BITS, 1>(down, a, lds, c, topk, hidden, inter, parts, room, pairs, partial, space);
+        down_body<BITS, 1>(down, a, lds, c, topk, hidden, inter, log_parts, room, pairs, partial, space);
 }
 
 // y = the weighted sum of a token's partial sums, its choices in order; a
@@ -1385,7 +1393,7 @@ sqllm_status products(const uint16_t *x, const int32_t *ids, const float *weight
         static std::atomic<uint64_t> asked{0};
         dev::raise_lds_limit((const void *)experts_down<BITS, MAXQ>, asked, (int)kStageRoom);
         hipLaunchKernelGGL((experts_down<BITS, MAXQ>), dim3(down_wgs, used, splits), threads, down_lds, stream, down, a, ids,
-                           batch, experts, topk, hidden, inter, down_parts, (int)down_lds, part);
+                           batch, experts, topk, hidden, inter, __builtin_ctz(down_parts), (int)down_lds, part);
     }
     hipLaunchKernelGGL(experts_combine, dim3(hidden / 256, batch), dim3(256), 0, stream, part, ids, weights, batch,
                        experts, topk, hidden, splits, y);

@@ -500,9 +500,9 @@ __device__ __forceinline__ void add_chunk(uint32_t val, float x, int cb, int v1,
 //     nonzero per lane (add_chunk): about 65 instructions a chunk and token,
 //     whatever the rows hold.
 // By rows unless the fullest row would take more than twice as many steps as
-// there are chunks (16 tokens, 128 experts 1536x4096 at 0.45%: gate and up 87
-// us by rows, 90 by chunks, 72 without outliers; 8 experts 3584x4096, 4 bits:
-// 40, 44 and 37).
+// there are chunks (us of a call by rows and by chunks: 16 tokens, 128 experts
+// 4096x1536 at 0.45% 154 and 159, at 2% 189 and 197; 8 experts 4096x3584, 4
+// bits, 57 and 60, 73 and 93, at 5% 98 and 166).
 struct Outliers {
     const uint16_t *cols, *vals; // the tile's
     int lo, count;               // this lane's row: entries [lo, lo + count)
@@ -1210,15 +1210,17 @@ int64_t used_at_most(int batch, int experts, int topk) { return batch * topk < e
 
 // Waves that share a down tile (8 waves to a workgroup): all eight while the
 // launch then fits the compute units at once (20 waves each).  Beyond that a
-// wave keeps at least three half groups, since finding its expert, its table
-// and the sums between waves cost it as much as three (16 tokens, 128 experts
-// 4096x1536: 82 us at eight waves, 61 at four, 60 at two, 67 at one; 8
-// experts 4096x3584: 27, 31, 49 and 88 us).
+// wave keeps at least three half groups, and fewer waves share a tile while
+// there are more than 40 a unit, since each has its expert to find, its table to
+// load and its sums to join (us of a call at 8, 4, 2 and 1: 16 tokens, 128
+// experts 4096x1536, 3 bits, 173, 151, 145, 139; 8 tokens, 128 experts 2048x768
+// 50, 45, 41, 44; 16 tokens, 64 experts 2048x2048, 2 bits, 51, 50, 52, 54; 8
+// experts 4096x3584 54, 55, 69, 98).
 int down_parts_for(int64_t tiles, int64_t inter)
 {
     int p = kDefaultWaves;
     if (tiles * p > 256 * 20)
-        while (p > 1 && inter / 128 < 3 * p) p /= 2;
+        while (p > 1 && (inter / 128 < 3 * p || tiles * p > 256 * 40)) p /= 2;
     return p;
 }
 

@@ -103,7 +103,9 @@ def choices(batch, experts, topk, seed):
 @pytest.mark.parametrize("batch,experts,topk,hidden,inter", [(1, 1, 1, 256, 256), (1, 8, 2, 512, 768), (2, 5, 3, 768, 512),
                                                              (4, 4, 4, 256, 1280), (5, 9, 2, 1024, 256), (8, 3, 2, 512, 256),
                                                              (9, 2, 1, 256, 512), (13, 6, 6, 512, 512), (16, 40, 8, 256, 256),
-                                                             (16, 1, 1, 512, 512), (3, 2, 2, 256, 4352), (1, 2, 1, 4608, 256)])
+                                                             (16, 1, 1, 512, 512), (3, 2, 2, 256, 4352), (1, 2, 1, 4608, 256),
+                                                             (16, 1, 1, 1280, 2304), (12, 2, 2, 2048, 2048), (16, 3, 1, 1024, 512),
+                                                             (16, 1, 1, 4096, 256), (7, 12, 4, 1792, 2048), (6, 150, 8, 2048, 512)])
 def test_experts(bits, batch, experts, topk, hidden, inter):
     step(f"moe experts {bits}-bit batch {batch} E {experts} K {topk} {hidden}x{inter}")
     layer = Layer(experts, hidden, inter, bits, batch + hidden)

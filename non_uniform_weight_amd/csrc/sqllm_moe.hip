@@ -966,8 +966,10 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up_table(P
     ChosenLds &lds = chosen[threadIdx.x >> 6];
     const Chosen c = find_chosen(ids, batch * topk, topk, batch, experts, blockIdx.y, lds);
     if (c.expert < 0) return;
+    // above eight tokens the table's answers and the sums do not fit the
+    // registers (16 tokens, 2 experts 4096x4096: 78 us a call, from registers 71)
     if (MAXQ >= 4 && c.count > 8)
-        gate_up_table_body<MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
+        gate_up_body<4, MAXQ >= 4 ? 4 : 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
     else if (MAXQ >= 2 && c.count > 4)
         gate_up_table_body<MAXQ >= 2 ? 2 : 1>(gate, up, x, lds, c, topk, hidden, inter, room, a, space);
     else

@@ -105,7 +105,8 @@ def choices(batch, experts, topk, seed):
                                                              (9, 2, 1, 256, 512), (13, 6, 6, 512, 512), (16, 40, 8, 256, 256),
                                                              (16, 1, 1, 512, 512), (3, 2, 2, 256, 4352), (1, 2, 1, 4608, 256),
                                                              (16, 1, 1, 1280, 2304), (12, 2, 2, 2048, 2048), (16, 3, 1, 1024, 512),
-                                                             (16, 1, 1, 4096, 256), (7, 12, 4, 1792, 2048), (6, 150, 8, 2048, 512)])
+                                                             (16, 1, 1, 4096, 256), (7, 12, 4, 1792, 2048), (6, 48, 8, 2048, 512),
+                                                             (16, 24, 4, 2048, 768)])
 def test_experts(bits, batch, experts, topk, hidden, inter):
     step(f"moe experts {bits}-bit batch {batch} E {experts} K {topk} {hidden}x{inter}")
     layer = Layer(experts, hidden, inter, bits, batch + hidden)
@@ -129,6 +130,14 @@ def test_outliers(bits, kw):
         x = tokens(batch, 512, 3)
         ids, weights = choices(batch, 3, 2, 4)
         layer.check(x, ids, weights, layer.run(x, ids, weights))
+
+
+def test_down_tiles_shared_by_four_waves():
+    step("moe down by four waves")
+    layer = Layer(22, 2048, 1536, 3, 29)
+    x = tokens(8, 2048, 30)
+    ids, weights = choices(8, 22, 4, 31)
+    layer.check(x, ids, weights, layer.run(x, ids, weights))
 
 
 @pytest.mark.parametrize("density", [0, 0.005])

@@ -996,11 +996,10 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_gate_up(Project
 
 // ---------------------------------------------------------------------------
 // part[split][pair][hidden] = down a, fp32, over the split's columns.  A
-// token j's two fp16 values stand in columns j and 2 NQ + j.  `parts` waves
-// share a tile and split.
-// Grid (ceil(hidden / 64 / (8 / parts)), experts in use at most, splits).
+// token j's two fp16 values stand in columns j and 2 NQ + j.
+// Grid (workgroups for hidden / 64 tiles, experts in use at most, splits).
 // ---------------------------------------------------------------------------
-// The same by pair tables: a tile to a workgroup.
+// By pair tables: eight waves share a tile.
 template <int BITS, int NQ>
 __device__ __forceinline__ void down_table_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
                                                 int topk, int hidden, int inter, int room, int64_t pairs,
@@ -1088,6 +1087,7 @@ __global__ void __launch_bounds__(kDefaultWaves * 64, 4) experts_down_table(Proj
         down_table_body<BITS, 1>(down, a, lds, c, topk, hidden, inter, room, pairs, partial, space);
 }
 
+// From registers: `parts` waves share a tile, so that a workgroup has 8 / parts.
 template <int BITS, int NQ>
 __device__ __forceinline__ void down_body(const Projection &down, Activations a, const ChosenLds &lds, Chosen c,
                                           int topk, int hidden, int inter, int log_parts, int room, int64_t pairs,

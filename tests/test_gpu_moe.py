@@ -6,6 +6,8 @@ sum is off by at most n 2^-23 M (its adds may truncate on the matrix cores).  Fo
 storing of a as two fp16 values).  A y is off by sum_k |w_k| (|down| da + n 2^-23 |down||a|), a few fp32 roundings of
 the sum over k (2^-20 of its magnitude) and its own rounding, 2^-11 |y| + 2^-25.  Router weights come from 64-bit
 scores: 2^-22 of the value covers the rounding to fp32."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -314,6 +316,27 @@ def test_layer_is_the_two_calls(small, batch):
     assert torch.equal(ids, rid) and torch.equal(weights, rw)
     assert torch.equal(y, small.run(x, rid, rw))
     small.check(x, ids, weights, y)
+
+
+def test_layers_from_two_threads_on_one_stream(small):
+    """The launches of a call that shares the stream's scratch stay together."""
+    step("moe two threads")
+    router = (torch.randn(300, 512, generator=torch.Generator().manual_seed(43)) / 16).half().cuda()
+    xs = [tokens(4, 512, 50 + i) for i in range(2)]
+    want = [nw().moe_route(x, router, 4) for x in xs]
+    bad = []
+
+    def run(i):
+        for _ in range(200):
+            ids, weights = nw().moe_route(xs[i], router, 4)
+            if not (torch.equal(ids, want[i][0]) and torch.equal(weights, want[i][1])):
+                bad.append(i)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
 
 
 def test_arguments_by_name(small):

@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -470,8 +471,8 @@ __global__ void __launch_bounds__(256) add_splits(const float *partial, int64_t 
     }
 }
 
-// Streaming form, for batches of at most 16: W is read once and everything
-// else hides behind that.  A wave takes 16 R rows of W and every waves-th
+// Streaming form, for batches of at most 16: W is read once and the rest hides
+// behind that.  A wave takes 16 R rows of W and every waves-th
 // block of columns, D steps of loads in flight; the waves' sums are added in
 // LDS.  W goes straight into LDS, each wave to a ring of its own (no barrier):
 // an instruction reads whole 128-byte lines of eight rows, where loads into
@@ -677,6 +678,22 @@ void launch_add(const Operands &p, int splits, const float *partial, hipStream_t
                        p.y);
 }
 
+// A small matrix for a few rows of x: the streaming form in one launch that
+// rounds x as it goes, while its workgroups fit the compute units at once (us at
+// batch 1, 8 and 16, and of the rounding and the tiled form: 4096x4096 8.9, 10.6
+// and 13.2, 10.9, 11.5 and 12.2; 1000x2048 4.9, 6.3 and 7.6, 8.9, 9.3 and 9.3;
+// but 28000x512 15.5, 22.7 and 31.7, 7.8, 7.9 and 8.2).
+bool fits_one_launch(int64_t rows, int64_t cols, int64_t batch)
+{
+    return batch <= 16 && rows <= 4096 && rows * cols <= 1 << 24;
+}
+
+// The streaming form for larger ones: where a wave has many blocks to read (us
+// of the streaming and the tiled form at batch 1 and 16: 8192x22016 38 and 49,
+// 45 and 52; 4096x11008 14 and 16, 16 and 17; 8192x8192 22 and 22, 24 and 23;
+// 12288x4096 21 and 16, 26 and 16; 16384x2048 13 and 11, 15 and 11).
+bool streams(int64_t cols, int64_t batch) { return batch <= 16 && cols > 8192; }
+
 // Splits of a streamed product's columns, up to 256 workgroups in all and two
 // blocks a wave at least.  Adding the sums up is a launch more, about 3.6 us of
 // the host's time, so only where the rows are few enough for it to save that
@@ -806,7 +823,9 @@ extern "C" sqllm_status sqllm_fp8_quantize(const uint16_t *x, int64_t rows, int6
 extern "C" size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
 {
     if (!good_shape(rows, cols) || !good_shape(batch, cols) || !good_product(rows, batch)) return 0;
-    const int splits = batch <= 16 ? stream_splits(rows, sqllm_fp8_cols(cols) / kBlock) : choose(rows, cols, batch).splits;
+    int splits = streams(cols, batch) ? 1 : choose(rows, cols, batch).splits;
+    if (streams(cols, batch) || fits_one_launch(rows, cols, batch))
+        splits = std::max(splits, stream_splits(rows, sqllm_fp8_cols(cols) / kBlock));
     return up256((size_t)batch * sqllm_fp8_cols(cols)) + up256((size_t)batch * sqllm_fp8_scale_pitch(cols)) +
            (splits > 1 ? (size_t)splits * batch * rows * 4 : 0);
 }
@@ -826,22 +845,18 @@ extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, i
     const Operands p = {q, scale, xq, xs, y, (int)rows, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
                         (int)sqllm_fp8_scale_pitch(cols)};
     float *partial = (float *)(xs + up256((size_t)batch * sqllm_fp8_scale_pitch(cols)));
-    // A small matrix for a few rows of x: one launch that rounds x as it goes
-    // (4096x4096 at batch 1, 8 and 16: 8.7, 10.3 and 13.2 us against 9.6, 11.7
-    // and 13.9 in two launches; 8192x4096 13.8, 17.5 and 23.1 against 13.2, 14.5
-    // and 15.9).
-    if (batch <= 16 && rows * cols <= 1 << 24 && aligned(x, 16) && cols % 8 == 0) {
+    if (fits_one_launch(rows, cols, batch) && aligned(x, 16) && cols % 8 == 0) {
         launch_stream<1, true>(p, x, (int)cols, partial, stream);
         return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
     }
     const sqllm_status st = quantize(x, batch, cols, cols, xq, xs, stream);
     if (st != SQLLM_OK) return st;
     // Two groups of 16 rows a wave halve the reads of x, where there are rows
-    // enough (8192x8192 at batch 1 and 16: 21.1 and 23.1 us against 20.2 and
-    // 30.1 with one group; 4096x8192: 15.1 and 19.0 against 12.8 and 18.3).
-    if (batch <= 16 && rows >= 8192)
+    // enough (8192x16384 at batch 1 and 16: 31 and 37 us against 40 and 52 with
+    // one group; 4096x22016: 28 and 38 against 22 and 28).
+    if (streams(cols, batch) && rows >= 8192)
         launch_stream<2, false>(p, x, (int)cols, partial, stream);
-    else if (batch <= 16)
+    else if (streams(cols, batch))
         launch_stream<1, false>(p, x, (int)cols, partial, stream);
     else
         launch_choice(choose(rows, cols, batch), p, partial, stream);

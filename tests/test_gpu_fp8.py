@@ -160,7 +160,8 @@ SHAPES = [(1, 1, 1), (1, 16, 128), (1, 300, 4096), (2, 129, 127), (3, 64, 8320),
           (1, 130, 20008), (11, 300, 24000), (16, 2000, 16500), (16, 8200, 512), (5, 8193, 300),
           (3600, 3590, 130), (3400, 3841, 640), (3585, 3500, 1000),
           (500, 6100, 300), (100, 300, 16500), (130, 129, 20000), (40, 200, 17000), (2, 8200, 2100), (16, 8193, 2176),
-          (9, 2050, 16400), (24, 2100, 5000), (90, 4100, 640)]
+          (9, 2050, 16400), (24, 2100, 5000), (90, 4100, 640), (16, 8200, 8200), (1, 8193, 9000), (5, 700, 8300),
+          (16, 4100, 4100), (3, 2000, 5001), (16, 6000, 700)]
 
 
 @pytest.mark.parametrize("batch,rows,cols", SHAPES)

@@ -131,12 +131,16 @@ __device__ __forceinline__ void choose(L logit, const float *bias, int experts, 
 #pragma unroll
         for (int j = 0; j < N; ++j) s[j] = 1.0 / (1.0 + exp(-s[j]));
     } else {
-        // exp(s - top) for any top near the largest: its upper half will do
-        uint32_t most = 0;
+        // the largest sum, exactly: its key's upper half, then the lower one among
+        // those (the upper half alone is off by up to 2^-20 of a sum, which from
+        // 2^30 on takes exponentials out of range)
+        uint64_t most = 0;
 #pragma unroll
-        for (int j = 0; j < N; ++j) most = max(most, (uint32_t)(order_key(s[j]) >> 32));
-        most = wave_max(most);
-        const double top = __longlong_as_double((long long)((uint64_t)(most >> 31 ? most ^ 0x80000000u : ~most) << 32));
+        for (int j = 0; j < N; ++j) most = max(most, order_key(s[j]));
+        const uint32_t hi = wave_max((uint32_t)(most >> 32));
+        const uint32_t lo = wave_max((uint32_t)(most >> 32) == hi ? (uint32_t)most : 0);
+        most = (uint64_t)hi << 32 | lo;
+        const double top = __longlong_as_double((long long)(most >> 63 ? most ^ 0x8000000000000000ull : ~most));
         double sum = 0.0;
 #pragma unroll
         for (int j = 0; j < N; ++j) {

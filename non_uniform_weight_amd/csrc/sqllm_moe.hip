@@ -188,7 +188,8 @@ __device__ __forceinline__ void choose(L logit, const float *bias, int experts, 
     }
     if (lane < topk) {
         ids[lane] = mine;
-        weights[lane] = (float)(kept * (flags & SQLLM_MOE_KEEP_SUM ? (double)scale : (double)scale / sum));
+        // the quotient first: 1 / sum is infinite where all scores are tiny
+        weights[lane] = (float)((flags & SQLLM_MOE_KEEP_SUM ? kept : kept / sum) * (double)scale);
     }
 }
 

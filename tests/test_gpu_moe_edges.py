@@ -28,3 +28,25 @@ def test_route_sums_beyond_a_billion(experts, sign):
     w = weights.cpu().numpy().astype(np.float64)
     np.testing.assert_array_equal(ids.cpu().numpy(), rid)
     assert (np.abs(w - rw) <= 2.0 ** -22 * rw).all()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_route_renormalizes_scores_near_the_smallest(sigmoid):
+    """A bias picks experts whose scores are around 1e-308 and below: their quotients are ordinary numbers.
+
+    The sums are exact.  Softmax scores from exp(-721), 7e-314, on hold 33 bits; a quotient's score and its sum are off by
+    less than 2^-30 each, and 2^-22 covers that and the rounding to fp32."""
+    step(f"moe route tiny scores, sigmoid {sigmoid}")
+    x = torch.zeros(2, 256, dtype=torch.float16, device="cuda")
+    router = torch.zeros(9, 256, dtype=torch.float16, device="cuda")
+    x[:, :2] = 1
+    router[1:, 0] = -708 if sigmoid else -720
+    router[1:, 1] = -(torch.arange(8) / (4 if sigmoid else 8)).half().cuda()
+    bias = torch.linspace(3, 2, 9).cuda()
+    bias[0] = -10
+    for scale in (1.0, 12.0):
+        rid, rw = route64(x, router, 2, bias, sigmoid, True, scale)
+        ids, weights = nw().moe_route(x, router, 2, bias=bias, sigmoid=sigmoid, scale=scale)
+        w = weights.cpu().numpy().astype(np.float64)
+        np.testing.assert_array_equal(ids.cpu().numpy(), rid)
+        assert np.isfinite(rw).all() and (np.abs(w - rw) <= 2.0 ** -22 * rw).all()

@@ -114,6 +114,20 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v)
     return __builtin_amdgcn_readlane(v, 63);
 }
 
+// The bits of all lanes' v, in every lane: the same.
+__device__ __forceinline__ uint32_t wave_or(uint32_t v)
+{
+#define SQLLM_OR_STEP(ctrl, rows) v |= (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, ctrl, rows, 0xF, true)
+    SQLLM_OR_STEP(0x111, 0xF); // row_shr 1, 2, 4, 8
+    SQLLM_OR_STEP(0x112, 0xF);
+    SQLLM_OR_STEP(0x114, 0xF);
+    SQLLM_OR_STEP(0x118, 0xF);
+    SQLLM_OR_STEP(0x142, 0xA); // row_bcast 15, 31
+    SQLLM_OR_STEP(0x143, 0xC);
+#undef SQLLM_OR_STEP
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
 // One wave's choice for one token; lane l holds experts l, l + 64, ... (N of
 // them; logit(e) is expert e's sum).  Each of the topk rounds takes the
 // largest key left, by its upper and then its lower half (ties: the lowest
@@ -478,31 +492,56 @@ __device__ __forceinline__ Chosen find_chosen(const int32_t *ids, int pairs, int
     return {e, (int)__popcll(tokens)};
 }
 
-// Adds one chunk of 64 nonzeros [cb, min(cb + 64, v1)) of a tile (lane's value
-// val and activation x; rows non-decreasing over the lanes) to the row lanes'
-// sums: an inclusive prefix sum over the wave, of which a row takes the
-// difference over its run of lanes [rp_lo, rp_hi).
-__device__ __forceinline__ void add_chunk(uint32_t val, float x, int cb, int v1, int lane, int rp_lo, int rp_hi, float &sum)
+// The pair (token, first choice) of an expert's token j, j the same in all
+// lanes: in scalar registers, where the addresses of sixteen tokens fit.
+__device__ __forceinline__ int64_t same_pair(const ChosenLds &lds, int j, int topk)
 {
-    float v = cb + lane < v1 ? dev::f16_to_f32((uint16_t)val) * x : 0.f;
-    v += dev::row_shr<1>(v);
-    v += dev::row_shr<2>(v);
-    v += dev::row_shr<4>(v);
-    v += dev::row_shr<8>(v);
-    v += dev::row_bcast15(v);
-    v += dev::row_bcast31(v);
-    const int first = max(rp_lo, cb) - cb, last = min(min(rp_hi, cb + 64), v1) - 1 - cb;
-    const bool present = first <= last;
-    const float top = dev::lane_read(present ? last : 0, v), below = dev::lane_read(present && first > 0 ? first - 1 : 0, v);
-    if (present) sum += first > 0 ? top - below : top;
+    const int at = __builtin_amdgcn_readfirstlane(lds.list[j]);
+    return (at & 255) * topk + (at >> 8);
 }
+
+// One chunk of 64 nonzeros [cb, min(cb + 64, v1)) of a tile: a nonzero per lane,
+// rows non-decreasing over the lanes, lanes past the end of no row; lane = row
+// has its row's entries [rp_lo, rp_hi).
+struct Chunk {
+    int back; // lanes before this one with nonzeros of the same row
+    int last; // lane of the last nonzero of this lane's row, -1 if it has none here
+
+    __device__ __forceinline__ void set(int cb, int v1, int lane, int rp_lo, int rp_hi)
+    {
+        const int first = max(rp_lo, cb) - cb, end = min(min(rp_hi, cb + 64), v1) - 1 - cb;
+        last = first <= end ? end : -1;
+        const uint64_t head = first <= end ? 1ull << first : 0; // first lanes of the rows here
+        const uint64_t heads = (uint64_t)wave_or((uint32_t)(head >> 32)) << 32 | wave_or((uint32_t)head);
+        back = lane - (63 - __clzll(heads & ((2ull << lane) - 1)));
+    }
+
+    // Adds the chunk (lane's product v) to the row lanes' sums: an
+    // inclusive scan over the wave that starts anew at each row, of which a row
+    // takes its last lane.  (The difference of an unbroken scan at a row's ends
+    // is two instructions a step less, but has the rounding errors of all rows
+    // before it in the chunk, and NaN after an infinity.)
+    __device__ __forceinline__ void add(float v, int lane, float &sum) const
+    {
+        int n = back;
+        asm("" : "+v"(n)); // compared anew for each token: the comparisons' masks do not fit the scalar registers
+        v += n >= 1 ? dev::row_shr<1>(v) : 0.f;
+        v += n >= 2 ? dev::row_shr<2>(v) : 0.f;
+        v += n >= 4 ? dev::row_shr<4>(v) : 0.f;
+        v += n >= 8 ? dev::row_shr<8>(v) : 0.f;
+        v += n > (lane & 15) ? dev::row_bcast15(v) : 0.f;
+        v += n > (lane & 31) ? dev::row_bcast31(v) : 0.f;
+        const float top = dev::lane_read(max(last, 0), v);
+        sum += last >= 0 ? top : 0.f;
+    }
+};
 
 // A wave's share of a tile's outliers, in one of two forms.
 //   By rows: lane = row takes entries 4 share .. 4 share + 3 of its row, then
 //     those 4 `shares` further, four at a load.  About 30 vector instructions
 //     a step and 8 a token.
 //   By chunks: an even part [v0, v1) of the tile's nonzeros, 64 at a time, a
-//     nonzero per lane (add_chunk): about 65 instructions a chunk and token,
+//     nonzero per lane (Chunk): about 65 instructions a chunk and token,
 //     whatever the rows hold.
 // By rows unless the fullest row would take more than twice as many steps as
 // there are chunks (us of a call by rows and by chunks: 16 tokens, 128 experts
@@ -576,12 +615,14 @@ struct Outliers {
         constexpr int kAtOnce = 2;
         for (int base = v0; base < v1; base += 64 * kAtOnce) {
             int col[kAtOnce];
-            uint32_t val[kAtOnce];
+            float val[kAtOnce];
+            Chunk chunk[kAtOnce];
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) { // past the last: that one again, dropped by add_chunk
+            for (int k = 0; k < kAtOnce; ++k) { // past the last: that one again, of no row
                 const int at = min(base + 64 * k + lane, v1 - 1);
                 col[k] = cols[at];
-                val[k] = vals[at];
+                val[k] = dev::f16_to_f32(vals[at]);
+                chunk[k].set(base + 64 * k, v1, lane, lo, lo + count);
             }
 #pragma unroll
             for (int j = 0; j < T; ++j)
@@ -591,8 +632,8 @@ struct Outliers {
                     for (int k = 0; k < kAtOnce; ++k) xv[k] = value(j, col[k]);
 #pragma unroll
                     for (int k = 0; k < kAtOnce; ++k)
-                        if (base + 64 * k < v1)
-                            add_chunk(val[k], xv[k], base + 64 * k, v1, lane, lo, lo + count, sum[j]);
+                        if (base + 64 * k < v1) chunk[k].add(val[k] * xv[k], lane, sum[j]);
+                    __builtin_amdgcn_sched_barrier(0); // (tokens interleaved do not fit the registers)
                 }
         }
     }
@@ -1045,7 +1086,7 @@ __device__ __forceinline__ void down_table_body(const Projection &down, Activati
     p.sums(sum);
     __syncthreads(); // the table is done with
     if (down.nnz > 0) { // (staged now, the table had the space)
-        auto whole_of = [&](int j) { return a.whole + pair_of(j) * inter; };
+        auto whole_of = [&](int j) { return a.whole + same_pair(lds, j, topk) * inter; };
         const bool staged = c.count * inter * 4 <= room;
         if (staged) {
             stage_rows(c.count, inter * 4, [&](int j) { return (const uint8_t *)whole_of(j); }, space);
@@ -1109,7 +1150,7 @@ __device__ __forceinline__ void down_body(const Projection &down, Activations a,
     float sum[4 * NQ];
     const int log_workers = log_parts + __builtin_ctz(gridDim.z), worker = blockIdx.z * parts + part;
     const int64_t lo_from_hi = a.lo - a.hi; // (a choice between the pointers puts them in scratch memory)
-    auto whole_of = [&](int j) { return a.whole + pair_of(j) * inter; };
+    auto whole_of = [&](int j) { return a.whole + same_pair(lds, j, topk) * inter; };
     const bool staged = c.count * inter * 4 <= room && down.nnz > 0;
     if (staged) stage_rows(c.count, inter * 4, [&](int j) { return (const uint8_t *)whole_of(j); }, space);
     Outliers out;

@@ -525,12 +525,14 @@ struct Chunk {
     {
         int n = back;
         asm("" : "+v"(n)); // compared anew for each token: the comparisons' masks do not fit the scalar registers
-        v += n >= 1 ? dev::row_shr<1>(v) : 0.f;
-        v += n >= 2 ? dev::row_shr<2>(v) : 0.f;
-        v += n >= 4 ? dev::row_shr<4>(v) : 0.f;
-        v += n >= 8 ? dev::row_shr<8>(v) : 0.f;
-        v += n > (lane & 15) ? dev::row_bcast15(v) : 0.f;
-        v += n > (lane & 31) ? dev::row_bcast31(v) : 0.f;
+        // (the shifts are calls, made by all lanes before any is chosen)
+        auto step = [&](bool same, float before) { v += same ? before : 0.f; };
+        step(n >= 1, dev::row_shr<1>(v));
+        step(n >= 2, dev::row_shr<2>(v));
+        step(n >= 4, dev::row_shr<4>(v));
+        step(n >= 8, dev::row_shr<8>(v));
+        step(n > (lane & 15), dev::row_bcast15(v));
+        step(n > (lane & 31), dev::row_bcast31(v));
         const float top = dev::lane_read(max(last, 0), v);
         sum += last >= 0 ? top : 0.f;
     }

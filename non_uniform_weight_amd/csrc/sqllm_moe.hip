@@ -592,10 +592,12 @@ struct Outliers {
             c >>= skip, v >>= skip;
             float w[4];
             int col[4];
+            bool own[4]; // entries past the row's count are other rows' and add nothing, whatever x holds there
 #pragma unroll
-            for (int k = 0; k < 4; ++k) { // entries past the row's count zero; their columns are some entry's
+            for (int k = 0; k < 4; ++k) {
                 col[k] = (int)(c >> (16 * k)) & 0xFFFF;
-                w[k] = first + k < count ? dev::f16_to_f32((uint16_t)(v >> (16 * k))) : 0.f;
+                w[k] = dev::f16_to_f32((uint16_t)(v >> (16 * k)));
+                own[k] = first + k < count;
             }
 #pragma unroll
             for (int j = 0; j < T; ++j)
@@ -604,7 +606,7 @@ struct Outliers {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) xv[k] = value(j, col[k]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) sum[j] += w[k] * xv[k];
+                    for (int k = 0; k < 4; ++k) sum[j] += own[k] ? w[k] * xv[k] : 0.f;
                 }
         }
     }

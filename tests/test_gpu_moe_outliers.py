@@ -71,3 +71,26 @@ def test_light_rows_beside_a_heavy_one(where, bits, hidden, inter):
         ids, weights = choices(batch, 2, 1, 4)
         weights *= 64
         layer.check(x, ids, weights, layer.run(x, ids, weights), floor=2.0 ** -36)
+
+
+@pytest.mark.parametrize("hidden,inter", [(512, 768), (1024, 512)])
+@pytest.mark.parametrize("bits", [2, 3, 4])
+@pytest.mark.parametrize("kw", [{"density": 0.005}, {"density": 0.01, "skew": True}])
+def test_an_infinite_x_gives_infinity(kw, bits, hidden, inter):
+    """One infinite entry of x among positive weights and activations: every sum of that token is infinite and none is
+    NaN, since no row meets another's column; the other tokens are as they were."""
+    step(f"moe infinite x {bits}-bit {kw} {hidden}x{inter}")
+    layer = Layer(3, hidden, inter, bits, 7, **kw)
+    for p in (layer.gate, layer.up, layer.down):
+        p.dev["lut"] = p.dev["lut"].abs() * 0.25 + 0.002
+        p.dev["val"] = p.dev["val"].abs() + 0.01
+    for batch in (2, 6, 16):
+        x = tokens(batch, hidden, 3).abs()
+        ids, weights = choices(batch, 3, 2, 4)
+        clean = layer.run(x, ids, weights)
+        assert clean.isfinite().all()
+        x[1, int(layer.gate.dev["col"][5].item())] = float("inf")
+        y = layer.run(x, ids, weights)
+        assert (y[1] == float("inf")).all(), f"{y[1].isnan().sum()} NaN"
+        keep = [t for t in range(batch) if t != 1]
+        assert torch.equal(y[keep], clean[keep])

@@ -217,13 +217,17 @@ __device__ __forceinline__ void wait_loads() // until at most N of this wave's l
     __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
 }
 
-// Barrier after which every wave's loads into LDS but its latest N are there.
-// (__syncthreads would wait for those N too: it is a fence for all memory.)
+// Barrier after which every wave's loads into LDS but its latest N are there, and
+// every wave's reads of LDS from before it are done: what it read may be loaded
+// over.  (__syncthreads would wait for those N too: it is a fence for all memory.
+// The wait for the reads is in one piece with the barrier, since the matrix steps
+// that use them, and with them the compiler's own wait, may be moved past it; at
+// present they are not, and it costs nothing.)
 template <int N>
 __device__ __forceinline__ void stage_barrier()
 {
     wait_loads<N>();
-    asm volatile("s_barrier" ::: "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // The tile of this workgroup: its first W row and x row; false if there is

@@ -682,16 +682,6 @@ void launch_add(const Operands &p, int splits, const float *partial, hipStream_t
                        p.y);
 }
 
-// A small matrix for a few rows of x: the streaming form in one launch that
-// rounds x as it goes, while its workgroups fit the compute units at once (us at
-// batch 1, 8 and 16, and of the rounding and the tiled form: 4096x4096 8.9, 10.6
-// and 13.2, 10.9, 11.5 and 12.2; 1000x2048 4.9, 6.3 and 7.6, 8.9, 9.3 and 9.3;
-// but 28000x512 15.5, 22.7 and 31.7, 7.8, 7.9 and 8.2).
-bool fits_one_launch(int64_t rows, int64_t cols, int64_t batch)
-{
-    return batch <= 16 && rows <= 4096 && rows * cols <= 1 << 24;
-}
-
 // The streaming form for larger ones: where a wave has many blocks to read (us
 // of the streaming and the tiled form at batch 1 and 16: 8192x22016 38 and 49,
 // 45 and 52; 4096x11008 14 and 16, 16 and 17; 8192x8192 22 and 22, 24 and 23;
@@ -711,6 +701,34 @@ int stream_splits(int64_t rows, int64_t blocks)
     int s = 1;
     while (s < 8 && rows * s < 16 * 256 && blocks >= 4 * s * kStreamWaves) s *= 2;
     return s;
+}
+
+// A small matrix for a few rows of x: the streaming form in one launch that
+// rounds x as it goes, while its workgroups fit the compute units at once.
+// Every workgroup rounds all of x again, so a wave has at most 60 blocks' rows
+// of x to round (or as many as that by compute unit, where there are more
+// workgroups than units).  us of this form and of rounding x with tiles or
+// streaming after it, replayed from a graph and, in brackets, back to back from
+// a host that takes 12 to 13 for two launches:
+//   1000x2048, 2 blocks a wave, batch 8 6.2 and 9.3 (7.6 and 10.7), 16 7.5 and
+//     9.3 (7.7 and 10.6)
+//   4096x4096, 4 blocks, 8 10.3 and 11.3 (10.2 and 12), 12 11.6 and 11.6 (11.5
+//     and 12), 16 13.2 and 12.0 (13.1 and 12)
+//   512x4096, 4 blocks, 12 10.6 and 10.1 (10.6 and 13), 16 12.2 and 10.5 (12.1
+//     and 13)
+//   2700x6016, 6 blocks, 8 10.3 and 11.9 (10.2 and 12), 12 12.0 and 12.2 (11.9
+//     and 12), 16 13.6 and 12.4 (13.5 and 12)
+//   2048x8192, 8 blocks, 1 11.4 and 10.4 (11.2 and 12), 4 12.1 and 10.6 (12.0
+//     and 13), 8 13.6 and 10.8 (13.6 and 13), 16 17.8 and 11.4 (17.7 and 13)
+//   1300x12800, 4 by compute unit, 8 15.0 and 15.0, 12 16.7 and 16.1, 16 18.6
+//     and 17.2
+//   28000x512, more rows than units, 1 15.5 and 7.8, 16 31.7 and 8.2
+bool fits_one_launch(int64_t rows, int64_t cols, int64_t batch)
+{
+    if (batch > 16 || rows > 4096 || rows * cols > 1 << 24) return false;
+    const int64_t blocks = sqllm_fp8_cols(cols) / kBlock;
+    const int64_t units = std::max<int64_t>(rows, 16 * 256 / stream_splits(rows, blocks)); // of 16 x 256
+    return batch * blocks * units <= 60 * kStreamWaves * 16 * 256;
 }
 
 template <int R, bool FUSED>

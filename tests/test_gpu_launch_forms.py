@@ -70,3 +70,16 @@ def test_more_large_tiles_than_compute_units(batch, rows, cols):
     y = nw().fp8_gemm(q, scale, x)
     check_product(q, scale, x, y)
     assert torch.equal(y, nw().fp8_gemm(q, scale, x))
+
+
+@pytest.mark.parametrize("rows,cols,batches", [(2048, 8192, (7, 8, 16)), (1300, 12800, (14, 15)), (2700, 6016, (10, 11)),
+                                               (500, 7168, (16,)), (4096, 4096, (15, 16)), (1600, 10240, (6, 7))])
+def test_small_matrices_on_both_sides_of_one_launch(rows, cols, batches):
+    """The streaming form that rounds x itself, up to the batch where the rounding outweighs a launch, and past it."""
+    q, scale = weights(rows, cols, 5)
+    for batch in batches:
+        step(f"fp8 gemm batch {batch} {rows}x{cols}")
+        x = acts(batch, cols, 6)
+        y = nw().fp8_gemm(q, scale, x)
+        check_product(q, scale, x, y)
+        assert torch.equal(y, nw().fp8_gemm(q, scale, x))

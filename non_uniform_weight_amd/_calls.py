@@ -14,6 +14,12 @@ import threading
 
 import torch
 
+
+def held(ctype, *values: int) -> bool:
+    """Whether the C type holds the values: ctypes cuts larger ones to their low bits without a word."""
+    return all(ctype(v).value == v for v in values)
+
+
 _SCRATCH: dict = {}
 # Several host threads may call on one stream: the launches of a call that uses the stream's buffer may not be
 # interleaved with another's.

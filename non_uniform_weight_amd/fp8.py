@@ -32,18 +32,18 @@ _gemm = _lib.sqllm_fp8_gemm
 @functools.lru_cache(maxsize=4096)
 def fp8_cols(cols: int) -> int:
     """Columns of the stored codes: cols rounded up to 128 (0 if out of range)."""
-    return int(_lib.sqllm_fp8_cols(cols))
+    return int(_lib.sqllm_fp8_cols(cols)) if _calls.held(_i64, cols) else 0
 
 
 @functools.lru_cache(maxsize=4096)
 def fp8_scale_pitch(cols: int) -> int:
     """Bytes of a row of scales: one per block of 128 columns, rounded up to 4 (0 if out of range)."""
-    return int(_lib.sqllm_fp8_scale_pitch(cols))
+    return int(_lib.sqllm_fp8_scale_pitch(cols)) if _calls.held(_i64, cols) else 0
 
 
 @functools.lru_cache(maxsize=4096)
 def fp8_workspace_bytes(rows: int, cols: int, batch: int) -> int:
-    return int(_lib.sqllm_fp8_workspace_bytes(rows, cols, batch))
+    return int(_lib.sqllm_fp8_workspace_bytes(rows, cols, batch)) if _calls.held(_i64, rows, cols, batch) else 0
 
 
 @_calls.on_stream

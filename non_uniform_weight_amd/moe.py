@@ -34,11 +34,14 @@ _lib.sqllm_moe_layer.argtypes = [_vp, _vp, _vp, _i32, _f32, _ep, _ep, _ep, _i32,
 
 EXPORTS = ("sqllm_moe_workspace_bytes", "sqllm_moe_route", "sqllm_moe_experts", "sqllm_moe_layer")
 _SIGMOID, _KEEP_SUM = 1, 2
+_MAX_TOPK, _ERR_SHAPE = 8, 3
 _route, _experts, _layer = _lib.sqllm_moe_route, _lib.sqllm_moe_experts, _lib.sqllm_moe_layer
 
 
 @functools.lru_cache(maxsize=4096)
 def moe_workspace_bytes(batch: int, experts: int, topk: int, hidden: int, inter: int) -> int:
+    if not (_calls.held(_i32, batch, experts, topk) and _calls.held(_i64, hidden, inter)):
+        return 0
     return int(_lib.sqllm_moe_workspace_bytes(batch, experts, topk, hidden, inter))
 
 
@@ -76,8 +79,10 @@ def _rows_of(x):
     return x.shape
 
 
-def _router(x, router, bias, index):
+def _router(x, router, bias, topk, index, call):
     batch, hidden = _rows_of(x)
+    if not 0 < topk <= _MAX_TOPK:  # before outputs of that width are made
+        _check(_ERR_SHAPE, call)
     rp = _calls.address(router, "router", torch.float16, index)
     if router.dim() != 2 or router.shape[1] != hidden:
         raise ValueError(f"router: shape (experts, {hidden}) expected, got {tuple(router.shape)}")
@@ -96,7 +101,7 @@ def moe_route(index, handle, x: torch.Tensor, router: torch.Tensor, topk: int, b
     """(ids int32, weights fp32), both [batch, topk]: each token's experts by softmax (or sigmoid) scores of
     x router^T.  bias (fp32 [experts]) moves the choice only; renormalize divides a token's weights by their sum.
     stream: as for every call (keyword)."""
-    batch, hidden, experts, rp, bp = _router(x, router, bias, index)
+    batch, hidden, experts, rp, bp = _router(x, router, bias, topk, index, "sqllm_moe_route")
     xp = _calls.address(x, "x", torch.float16, index)
     flags = (_SIGMOID if sigmoid else 0) | (0 if renormalize else _KEEP_SUM)
     ids, ip = _calls.output(ids, "ids", (batch, topk), torch.int32, index)
@@ -132,7 +137,7 @@ def moe_layer(index, handle, x: torch.Tensor, router: torch.Tensor, topk: int, g
               y: torch.Tensor | None = None, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
               ws: torch.Tensor | None = None):
     """(y, ids, weights): moe_route and moe_experts in one call."""
-    batch, hidden, experts, rp, bp = _router(x, router, bias, index)
+    batch, hidden, experts, rp, bp = _router(x, router, bias, topk, index, "sqllm_moe_layer")
     inter = gate["lut"].shape[1]
     g, u, d = _projections(gate, up, down, bits, experts, hidden, inter, index)
     xp = _calls.address(x, "x", torch.float16, index)

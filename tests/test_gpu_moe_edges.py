@@ -50,3 +50,11 @@ def test_route_renormalizes_scores_near_the_smallest(sigmoid):
         w = weights.cpu().numpy().astype(np.float64)
         np.testing.assert_array_equal(ids.cpu().numpy(), rid)
         assert np.isfinite(rw).all() and (np.abs(w - rw) <= 2.0 ** -22 * rw).all()
+
+
+@pytest.mark.parametrize("topk", [0, -1, 9, 2 ** 32 + 2])
+def test_route_refuses_topk_before_any_output(topk):
+    step(f"moe route topk {topk}")
+    x, router = (torch.zeros(n, 256, dtype=torch.float16, device="cuda") for n in (2, 16))
+    with pytest.raises(nw().SqllmError, match="moe_route"):
+        nw().moe_route(x, router, topk)

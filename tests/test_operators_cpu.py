@@ -75,6 +75,19 @@ def test_moe_sizes(nw):
         assert size(**bad) == 0, bad
 
 
+def test_sizes_beyond_the_c_types(nw):
+    """Sizes that the low bits alone would make good ones."""
+    assert nw.fp8_cols(2 ** 64 + 5) == nw.fp8_scale_pitch(2 ** 64 + 5) == nw.fp8_cols(5 - 2 ** 64) == 0
+    for at in range(3):
+        sizes = [64, 1000, 33]
+        sizes[at] += 2 ** 64
+        assert nw.fp8_workspace_bytes(*sizes) == 0
+    for at in range(5):
+        sizes = [4, 8, 2, 512, 768]
+        sizes[at] += 2 ** 32 if at < 3 else 2 ** 64
+        assert nw.moe_workspace_bytes(*sizes) == 0
+
+
 def projection(nw, **kw):
     f = dict(packed=A.value, lut=B.value, row_ptr=A.value, col_idx=A.value, val=A.value, nnz=10)
     return nw.moe.Experts(**{**f, **kw})

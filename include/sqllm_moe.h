@@ -59,9 +59,10 @@ typedef struct {
     const void *packed;      /* [experts] packed matrices of sqllm_packed_bytes() each, 16-byte aligned */
     const uint16_t *lut;     /* fp16 [experts][rows][2^bits], 16-byte aligned */
     const int32_t *row_ptr;  /* int32 [experts * rows + 1]: one CSR over the experts' rows in order */
-    const uint16_t *col_idx; /* uint16 [nnz], < cols */
+    const uint16_t *col_idx; /* uint16 [nnz], < cols in the rows' entries */
     const uint16_t *val;     /* fp16 [nnz] */
-    int64_t nnz;             /* 0: no outliers (row_ptr, col_idx and val may be NULL) */
+    int64_t nnz;             /* 0: no outliers (row_ptr, col_idx and val may be NULL); at least row_ptr's last
+                              * entry, what the arrays hold behind it is of no row */
 } sqllm_experts;
 
 /* Scratch bytes that every call below needs at most for these sizes; 0 if

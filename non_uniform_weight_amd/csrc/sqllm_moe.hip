@@ -592,12 +592,14 @@ struct Outliers {
             c >>= skip, v >>= skip;
             float w[4];
             int col[4];
-            bool own[4]; // entries past the row's count are other rows' and add nothing, whatever x holds there
+            // Entries past the row's count are other rows' or, at the arrays' end,
+            // nobody's: they read x in column 0 and add nothing, whatever it holds.
+            bool own[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                col[k] = (int)(c >> (16 * k)) & 0xFFFF;
-                w[k] = dev::f16_to_f32((uint16_t)(v >> (16 * k)));
                 own[k] = first + k < count;
+                col[k] = own[k] ? (int)(c >> (16 * k)) & 0xFFFF : 0;
+                w[k] = dev::f16_to_f32((uint16_t)(v >> (16 * k)));
             }
 #pragma unroll
             for (int j = 0; j < T; ++j)

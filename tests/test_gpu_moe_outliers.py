@@ -94,3 +94,18 @@ def test_an_infinite_x_gives_infinity(kw, bits, hidden, inter):
         assert (y[1] == float("inf")).all(), f"{y[1].isnan().sum()} NaN"
         keep = [t for t in range(batch) if t != 1]
         assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4])
+def test_arrays_longer_than_the_rows_entries(bits):
+    """Behind the last row's entries the arrays may hold anything: it is of no row."""
+    step(f"moe outlier arrays with a tail, {bits}-bit")
+    layer = Layer(2, 512, 768, bits, 9, density=0.004)
+    for p in (layer.gate, layer.up, layer.down):
+        for name, fill in (("col", -1), ("val", float("nan"))):
+            t = p.dev[name]
+            p.dev[name] = torch.cat([t, torch.full((37,), fill, dtype=t.dtype, device="cuda")])
+    for batch in (1, 6, 16):
+        x = tokens(batch, 512, 3)
+        ids, weights = choices(batch, 2, 1, 4)
+        layer.check(x, ids, weights, layer.run(x, ids, weights))

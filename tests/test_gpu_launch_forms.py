@@ -83,3 +83,79 @@ def test_small_matrices_on_both_sides_of_one_launch(rows, cols, batches):
         y = nw().fp8_gemm(q, scale, x)
         check_product(q, scale, x, y)
         assert torch.equal(y, nw().fp8_gemm(q, scale, x))
+
+
+def test_weights_past_four_gigabytes():
+    """300000 x 16384 in 8 bits, 4.9 GB: the last rows' codes and products."""
+    base = (torch.randn(1000, 16384, generator=torch.Generator().manual_seed(1)) * 0.02).half().cuda()
+    step("fp8 quantize 300000x16384")
+    q, scale = nw().fp8_quantize(base.repeat(300, 1))
+    want, wscale = nw().fp8_quantize(base)
+    assert torch.equal(q[-1000:], want) and torch.equal(scale[-1000:], wscale)
+    for batch in (1, 16, 40, 300):
+        step(f"fp8 gemm batch {batch} 300000x16384")
+        x = acts(batch, 16384, batch)
+        y = nw().fp8_gemm(q, scale, x)
+        check_product(want, wscale, x, y[:, -1000:].contiguous())
+
+
+@pytest.mark.parametrize("bits,experts", [(3, 200), (4, 136)])
+def test_experts_past_four_gigabytes(bits, experts):
+    """Copies of one expert of 8192x8192, more than 4 GB a projection: the last one's y is the first one's."""
+    r = np.random.default_rng(bits)
+    parts = {}
+    for name in ("gate", "up", "down"):
+        codes = torch.from_numpy(r.integers(0, 1 << bits, (8192, 8192), dtype=np.uint8)).cuda()
+        lut = torch.from_numpy((r.standard_normal((1, 8192, 1 << bits)) * 0.02).astype(np.float16)).cuda()
+        counts = r.binomial(8192, 0.001, 8192)
+        nnz = int(counts.sum())
+        row_ptr = np.concatenate([[0], np.cumsum(np.tile(counts, experts))])
+        col, val = r.integers(0, 8192, nnz).astype(np.uint16), (r.standard_normal(nnz) * 0.1).astype(np.float16)
+        parts[name] = {"packed": nw().pack(codes, bits).repeat(experts), "lut": lut.repeat(experts, 1, 1),
+                       "row_ptr": torch.from_numpy(row_ptr.astype(np.int32)).cuda(),
+                       "col": torch.from_numpy(col.view(np.int16)).cuda().repeat(experts),
+                       "val": torch.from_numpy(val).cuda().repeat(experts)}
+        assert parts[name]["packed"].numel() > 1 << 32
+    for batch in (1, 9):
+        step(f"moe experts {bits}-bit batch {batch} {experts} of 8192x8192")
+        x = tokens(batch, 8192, 3)
+        w = torch.ones(batch, 1, device="cuda")
+        first = nw().moe_experts(x, torch.zeros(batch, 1, dtype=torch.int32, device="cuda"), w, **parts, bits=bits)
+        last = nw().moe_experts(x, torch.full((batch, 1), experts - 1, dtype=torch.int32, device="cuda"), w, **parts, bits=bits)
+        assert first.isfinite().all() and first.abs().max() > 0 and torch.equal(first, last)
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls that follow each other on two streams with nothing between them: each stream has scratch of its own."""
+    step("two streams at once")
+    layer = Layer(7, 512, 768, 3, 23)
+    router = (tokens(7, 512, 42).float() / 512 ** 0.5).half()
+    q, scale = weights(1000, 512, 4)
+
+    def step_of(x, **kw):
+        y = nw().moe_layer(x, router, 2, layer.gate.dev, layer.up.dev, layer.down.dev, 3, **kw)[0]
+        return y, nw().fp8_gemm(q, scale, x, **kw)
+
+    xs = [tokens(b, 512, 50 + b) for b in (3, 16)]
+    want = [step_of(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [(k, step_of(xs[k], stream=streams[k])) for _ in range(40) for k in range(2)]
+    torch.cuda.synchronize()
+    for k, out in got:
+        assert all(torch.equal(a, b) for a, b in zip(out, want[k]))
+
+
+def test_quantize_in_a_graph():
+    step("fp8 quantize captured")
+    x = torch.from_numpy(wide(33, 700, 1)).cuda()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q, scale = nw().fp8_quantize(x)
+    for seed in (2, 3, 4):
+        xh = wide(33, 700, seed)
+        x.copy_(torch.from_numpy(xh))
+        g.replay()
+        torch.cuda.synchronize()
+        check_quantized(xh, q, scale)

@@ -541,14 +541,15 @@ struct Chunk {
 // A wave's share of a tile's outliers, in one of two forms.
 //   By rows: lane = row takes entries 4 share .. 4 share + 3 of its row, then
 //     those 4 `shares` further, four at a load.  About 30 vector instructions
-//     a step and 8 a token.
+//     a step and 12 a token.
 //   By chunks: an even part [v0, v1) of the tile's nonzeros, 64 at a time, a
-//     nonzero per lane (Chunk): about 65 instructions a chunk and token,
-//     whatever the rows hold.
+//     nonzero per lane (Chunk): about 40 vector instructions a chunk and 35 a
+//     token, whatever the rows hold.
 // By rows unless the fullest row would take more than twice as many steps as
-// there are chunks (us of a call by rows and by chunks: 16 tokens, 128 experts
-// 4096x1536 at 0.45% 154 and 159, at 2% 189 and 197; 8 experts 4096x3584, 4
-// bits, 57 and 60, 73 and 93, at 5% 98 and 166).
+// there are chunks (us of a call by rows and by chunks, replayed from a graph:
+// 16 tokens, 128 experts 4096x1536 at 0.45% 148 and 159, at 2% 211 and 231; 8
+// experts 4096x3584, 4 bits, 58 and 62, 71 and 96, at 5% 96 and 172; 8 tokens,
+// 128 experts 2048x768, 4 bits, 57 and 57, 61 and 68).
 struct Outliers {
     const uint16_t *cols, *vals; // the tile's
     int lo, count;               // this lane's row: entries [lo, lo + count)
@@ -653,7 +654,8 @@ template <int BITS, int NQ, typename X>
 __device__ __forceinline__ void tile_product(const Projection &p, int64_t tile, int groups, int worker, int log_workers, X x,
                                              float (&sum)[4 * NQ], Outliers &out)
 {
-    // half groups in flight, as many as fit 128 registers without spilling
+    // half groups in flight, as many as fit 128 registers (with sums of sixteen
+    // tokens, NQ = 8, even one spills four to seven of them)
     constexpr int D = NQ == 1 ? (BITS == 2 ? 3 : 4) : (NQ == 2 ? (BITS == 2 ? 2 : 3) : (NQ == 4 && BITS == 3 ? 2 : 1));
     constexpr int C = NQ == 1 ? 2 : 1; // accumulator chains: a step does not wait for the one before it
     const int lane = threadIdx.x & 63, block = lane >> 2;

@@ -68,6 +68,16 @@ size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
 sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols, const uint16_t *x,
                             int64_t batch, uint16_t *y, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * sqllm_fp8_gemm_stored -- the same with x already in the stored form, as
+ * sqllm_fp8_quantize and sqllm_rms_norm_fp8 leave it: xq uint8 [batch]
+ * [sqllm_fp8_cols(cols)], 16-byte aligned, xscale uint8 [batch]
+ * [sqllm_fp8_scale_pitch(cols)], 4-byte aligned.
+ */
+sqllm_status sqllm_fp8_gemm_stored(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
+                                   const uint8_t *xq, const uint8_t *xscale, int64_t batch, uint16_t *y,
+                                   void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -432,4 +432,7 @@ def algorithmic_bytes(rows: int, cols: int, bits: int, nnz: int, batch: int) -> 
 
 # Calls with ABI headers of their own (they use the names above).
 from .fp8 import fp8_cols, fp8_gemm, fp8_quantize, fp8_scale_pitch, fp8_workspace_bytes  # noqa: E402
+from .int8 import (int8_cols, int8_gemm, int8_glu, int8_glu_workspace_bytes, int8_quantize,  # noqa: E402
+                   int8_workspace_bytes)
 from .moe import moe_experts, moe_layer, moe_route, moe_workspace_bytes  # noqa: E402
+from .norm import rms_norm, rms_norm_fp8, rms_norm_int8  # noqa: E402

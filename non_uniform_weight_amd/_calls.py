@@ -57,6 +57,24 @@ def _checked_address(t, name: str, dtype, index: int) -> int:
     return t.data_ptr()
 
 
+def half_rows(x, name: str, index: int):
+    """(rows, columns, values from a row to the next, address) of fp16 x [rows, cols], its columns adjacent."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: torch.Tensor expected")
+    if x.dim() != 2 or x.numel() == 0:
+        raise ValueError(f"{name}: shape (rows, cols) expected, got {tuple(x.shape)}")
+    if x.get_device() != index:
+        raise ValueError(f"{name}: on {x.device}, the call's other tensors on cuda:{index}")
+    if x.dtype is not torch.float16:
+        raise TypeError(f"{name}: dtype torch.float16 expected, got {x.dtype}")
+    rows, cols = x.shape
+    if x.is_contiguous():
+        return rows, cols, cols, x.data_ptr()
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError(f"{name}: adjacent columns expected")
+    return rows, cols, x.stride(0) if rows > 1 else cols, x.data_ptr()
+
+
 def output(t, name: str, shape: tuple, dtype, index: int):
     """(t, its address); a new tensor where t is None.  Called with the call's stream current."""
     if t is None:

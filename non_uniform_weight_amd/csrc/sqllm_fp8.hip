@@ -852,17 +852,46 @@ extern "C" size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t 
            (splits > 1 ? (size_t)splits * batch * rows * 4 : 0);
 }
 
-extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
-                                       const uint16_t *x, int64_t batch, uint16_t *y, void *workspace,
-                                       size_t workspace_bytes, hipStream_t stream)
+namespace {
+
+// What both products check alike; x: in either form, aligned to x_align.
+sqllm_status check_product(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols, const void *x,
+                           uintptr_t x_align, int64_t batch, const uint16_t *y, const void *workspace,
+                           size_t workspace_bytes)
 {
     if (!q || !scale || !x || !y) return SQLLM_ERR_NULL;
     if (!good_shape(rows, cols)) return SQLLM_ERR_SHAPE;
     if (!good_shape(batch, cols)) return SQLLM_ERR_BATCH;
     if (!good_product(rows, batch)) return SQLLM_ERR_SHAPE;
-    if (!aligned(q, 16) || !aligned(scale, 4) || !aligned(x, 2) || !aligned(y, 2)) return SQLLM_ERR_ALIGN;
+    if (!aligned(q, 16) || !aligned(scale, 4) || !aligned(x, x_align) || !aligned(y, 2)) return SQLLM_ERR_ALIGN;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < sqllm_fp8_workspace_bytes(rows, cols, batch))
         return SQLLM_ERR_WORKSPACE;
+    return SQLLM_OK;
+}
+
+// The product of operands in the stored form.
+sqllm_status launch_product(const Operands &p, int64_t cols, float *partial, hipStream_t stream)
+{
+    // Two groups of 16 rows a wave halve the reads of x, where there are rows
+    // enough (8192x16384 at batch 1 and 16: 31 and 37 us against 40 and 52 with
+    // one group; 4096x22016: 28 and 38 against 22 and 28).
+    if (streams(cols, p.batch) && p.rows >= 8192)
+        launch_stream<2, false>(p, nullptr, (int)cols, partial, stream);
+    else if (streams(cols, p.batch))
+        launch_stream<1, false>(p, nullptr, (int)cols, partial, stream);
+    else
+        launch_choice(choose(p.rows, cols, p.batch), p, partial, stream);
+    return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
+}
+
+} // namespace
+
+extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
+                                       const uint16_t *x, int64_t batch, uint16_t *y, void *workspace,
+                                       size_t workspace_bytes, hipStream_t stream)
+{
+    sqllm_status st = check_product(q, scale, rows, cols, x, 2, batch, y, workspace, workspace_bytes);
+    if (st != SQLLM_OK) return st;
     uint8_t *xq = (uint8_t *)workspace, *xs = xq + up256((size_t)batch * sqllm_fp8_cols(cols));
     const Operands p = {q, scale, xq, xs, y, (int)rows, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
                         (int)sqllm_fp8_scale_pitch(cols)};
@@ -871,16 +900,20 @@ extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, i
         launch_stream<1, true>(p, x, (int)cols, partial, stream);
         return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
     }
-    const sqllm_status st = quantize(x, batch, cols, cols, xq, xs, stream);
+    st = quantize(x, batch, cols, cols, xq, xs, stream);
+    return st != SQLLM_OK ? st : launch_product(p, cols, partial, stream);
+}
+
+extern "C" sqllm_status sqllm_fp8_gemm_stored(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
+                                              const uint8_t *xq, const uint8_t *xscale, int64_t batch, uint16_t *y,
+                                              void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (!xscale) return SQLLM_ERR_NULL;
+    const sqllm_status st = check_product(q, scale, rows, cols, xq, 16, batch, y, workspace, workspace_bytes);
     if (st != SQLLM_OK) return st;
-    // Two groups of 16 rows a wave halve the reads of x, where there are rows
-    // enough (8192x16384 at batch 1 and 16: 31 and 37 us against 40 and 52 with
-    // one group; 4096x22016: 28 and 38 against 22 and 28).
-    if (streams(cols, batch) && rows >= 8192)
-        launch_stream<2, false>(p, x, (int)cols, partial, stream);
-    else if (streams(cols, batch))
-        launch_stream<1, false>(p, x, (int)cols, partial, stream);
-    else
-        launch_choice(choose(rows, cols, batch), p, partial, stream);
-    return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
+    if (!aligned(xscale, 4)) return SQLLM_ERR_ALIGN;
+    const Operands p = {q, scale, xq, xscale, y, (int)rows, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
+                        (int)sqllm_fp8_scale_pitch(cols)};
+    // (the query's bytes hold the two parts of x first, here unused)
+    return launch_product(p, cols, (float *)workspace, stream);
 }

@@ -1,0 +1,378 @@
+// sqllm_int8.hip -- the products of include/sqllm_int8.h: argument checks,
+// kernels and launches.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "sqllm_device.h"
+#include "sqllm_int8.h"
+#include "sqllm_rows.h"
+
+namespace {
+
+constexpr int kBlock = 128; // columns of a stage
+using sqllm::dev::u32x2;
+using sqllm::dev::u32x4;
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+
+// ---------------------------------------------------------------------------
+// v_mfma_i32_16x16x64_i8: lane l gives 16 bytes of row l % 16 of A (here W)
+// and of B (here x).  The instruction sums over all 64 positions, so any order
+// of the columns will do as long as A and B agree.  Register i of lane l holds
+// the sum of W row 4 (l / 16) + i and x row l % 16.  All sums are exact, so
+// their order, and how the columns are split, does not show in the result.
+// ---------------------------------------------------------------------------
+
+// One product of W rows with x rows, or (gated) two with the same x.
+struct Operands {
+    const int8_t *wq[2];
+    const float *wscale[2];
+    const int8_t *xq;
+    const float *xscale;
+    uint16_t *y;
+    int rows, batch, blocks;
+};
+
+// Every rounding that the header names is made, in every form of a product: v
+// is a number in fp32 before it is rounded to fp16 (the compiler would fuse the
+// multiply before it with the rounding in some places and not in others).
+__device__ __forceinline__ uint16_t half_of(float v)
+{
+    asm("" : "+v"(v));
+    return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+
+// A sum as a number; silu(g) u.
+__device__ __forceinline__ float scaled(int sum, float xs, float ws) { return (float)sum * (xs * ws); }
+__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+
+// Four W rows r..r+3 of one x row, rounded once; in one store where the row of
+// y is aligned for it.
+__device__ __forceinline__ void store4(const Operands &p, int b, int r, const float (&v)[4])
+{
+    if (b >= p.batch || r >= p.rows) return;
+    uint16_t *y = p.y + (int64_t)b * p.rows + r;
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = half_of(v[i]);
+    if (r + 4 <= p.rows && ((uintptr_t)y & 7) == 0) {
+        *(u32x2 *)y = u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r + i < p.rows) y[i] = h[i];
+}
+
+// Sums of W rows r..r+3 with x row b, of one or both products, to y.
+template <bool GLU>
+__device__ __forceinline__ void finish4(const Operands &p, int b, int r, i32x4 g, i32x4 u)
+{
+    if (b >= p.batch || r >= p.rows) return;
+    const float xs = p.xscale[b];
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int at = min(r + i, p.rows - 1);
+        v[i] = scaled(g[i], xs, p.wscale[0][at]);
+        if constexpr (GLU) v[i] = gated(v[i], scaled(u[i], xs, p.wscale[1][at]));
+    }
+    store4(p, b, r, v);
+}
+
+// The same of split blockIdx.y, as sums: partial[split][product][batch][rows].
+template <bool GLU>
+__device__ __forceinline__ void store_partial(const Operands &p, int *partial, int b, int r, i32x4 g, i32x4 u)
+{
+    if (b >= p.batch) return;
+    const int64_t size = (int64_t)p.batch * p.rows;
+    int *at = partial + blockIdx.y * (GLU ? 2 : 1) * size + (int64_t)b * p.rows + r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (r + i < p.rows) {
+            at[i] = g[i];
+            if constexpr (GLU) at[size + i] = u[i];
+        }
+}
+
+// Each lane's 16 bytes at src to lds_base + 16 * lane.
+__device__ __forceinline__ void lds_load16(const int8_t *src, int8_t *lds_base)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) uint32_t *)src,
+                                     (__attribute__((address_space(3))) uint32_t *)lds_base, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() // until at most N of this wave's loads are in flight
+{
+    static_assert(N < 64, "vmcnt");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
+}
+
+// Barrier after which every wave's loads into LDS but its latest N are there, and
+// every wave's reads of LDS from before it are done: what it read may be loaded
+// over.  (The wait for the reads is in one piece with the barrier, since the
+// matrix steps that use them, and with them the compiler's own wait, may be
+// moved past it.)
+template <int N>
+__device__ __forceinline__ void stage_barrier()
+{
+    wait_loads<N>();
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// The tile of this workgroup: its first W row and x row; false if there is
+// none.  Workgroups go round the eight XCDs: each gets a run of tiles, four W
+// tiles wide, so that the 32 it works on at once share their rows in its L2.
+template <int TM, int TN>
+__device__ __forceinline__ bool tile_of(const Operands &p, int &r0, int &b0)
+{
+    constexpr int G = 4;
+    const int mt = (p.rows + TM - 1) / TM, nt = (p.batch + TN - 1) / TN, tiles = mt * nt;
+    const int per = (tiles + 7) / 8, id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || id >= tiles) return false;
+    const int group = id / (G * nt), in = id - group * (G * nt), width = min(G, mt - group * G);
+    r0 = (group * G + in % width) * TM;
+    b0 = (in / width) * TN;
+    return true;
+}
+
+// Tiled form.  A workgroup computes TM rows of W (gated: TM / 2 of each matrix)
+// by TN rows of x over the blocks of its split, each wave WM by WN of them in
+// 16x16 accumulators (gated: WM / 2 rows of gate and the same of up, so that a
+// lane holds both sums of a place).  Both operands go through LDS, one block a
+// stage, S stages in turn: loads go straight from memory into LDS, S - 1
+// stages ahead of the matrix cores, and one barrier a stage separates them.
+// Every wave issues the same number of loads in every stage (past the last
+// block it reads that again), so that the count of loads in flight says which
+// stage has arrived.  A row's eight 16-byte pieces are stored at piece ^
+// (row % 8), so that the sixteen rows that a fragment read takes at one piece
+// lie in different banks; loads into LDS write lane after lane, so the swizzle
+// is in the address they read from.
+template <int TM, int TN, int WM, int WN, int S>
+struct Tiling {
+    static constexpr int W = (TM / WM) * (TN / WN);
+    static constexpr int kData = (TM + TN) * kBlock;
+    static constexpr int kLoads = (TM + TN) / 8 / W; // 1 KB each
+    static constexpr size_t kLds = (size_t)S * kData;
+    static_assert((TM + TN) / 8 % W == 0, "as many loads in every wave");
+    static_assert(TM % 16 == 0 && WM % 32 == 0, "halves of whole loads and accumulators");
+};
+
+template <bool GLU, int TM, int TN, int WM, int WN, int S>
+__global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Operands p, int splits, int *partial)
+{
+    using T = Tiling<TM, TN, WM, WN, S>;
+    constexpr int kRows = GLU ? TM / 2 : TM; // of a matrix
+    extern __shared__ __align__(16) int8_t lds[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, quarter = lane >> 4;
+    int r0, b0;
+    if (!tile_of<kRows, TN>(p, r0, b0)) return;
+    const int share = (p.blocks + splits - 1) / splits, k0 = blockIdx.y * share, k1 = min(k0 + share, p.blocks);
+    if (k0 >= k1) return; // (the host leaves no split empty)
+
+    // this wave's loads: 8 rows each of one operand; lane l reads piece
+    // (l % 8) ^ (l / 8) of row l / 8.  Offsets from the tile's first row fit
+    // 32 bits (255 rows of at most 2^17 columns).
+    const uint32_t ld = (uint32_t)p.blocks * kBlock;
+    const int8_t *src[T::kLoads];
+    uint32_t from[T::kLoads];
+#pragma unroll
+    for (int i = 0; i < T::kLoads; ++i) { // rows past the end: copies of the last
+        const int first = (w * T::kLoads + i) * 8, row = first + (lane >> 3);
+        int at;
+        if (first >= TM) {
+            src[i] = p.xq + (int64_t)b0 * ld;
+            at = min(row - TM, p.batch - 1 - b0);
+        } else if constexpr (GLU) {
+            src[i] = (first % WM >= WM / 2 ? p.wq[1] : p.wq[0]) + (int64_t)r0 * ld;
+            at = min(row / WM * (WM / 2) + row % (WM / 2), p.rows - 1 - r0);
+        } else {
+            src[i] = p.wq[0] + (int64_t)r0 * ld;
+            at = min(row, p.rows - 1 - r0);
+        }
+        from[i] = (uint32_t)at * ld + ((lane & 7) ^ (lane >> 3)) * 16;
+    }
+    auto load_stage = [&](int k, int slot) {
+        const int at = min(k, k1 - 1);
+#pragma unroll
+        for (int i = 0; i < T::kLoads; ++i)
+            lds_load16(src[i] + (uint32_t)at * kBlock + from[i], lds + slot * T::kData + (w * T::kLoads + i) * 1024);
+    };
+
+    constexpr int FM = WM / 16, FN = WN / 16;
+    const int wm = (w % (TM / WM)) * WM, wn = (w / (TM / WM)) * WN;
+    i32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    const int piece = n * kBlock + ((quarter ^ (n & 7)) * 16);
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) load_stage(k0 + s, s);
+    int slot = 0;
+    for (int k = k0; k < k1; ++k) {
+        stage_barrier<(S - 2) * T::kLoads>(); // stage k is in LDS
+        load_stage(k + S - 1, slot == 0 ? S - 1 : slot - 1); // where stage k - 1 was
+        const int8_t *base = lds + slot * T::kData;
+        slot = slot == S - 1 ? 0 : slot + 1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) { // 64 columns: pieces 4 h + quarter
+            const int8_t *at = base + (piece ^ (64 * h));
+            i32x4 b[FN];
+#pragma unroll
+            for (int j = 0; j < FN; ++j) b[j] = *(const i32x4 *)(at + (TM + wn + 16 * j) * kBlock);
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const i32x4 a = *(const i32x4 *)(at + (wm + 16 * i) * kBlock);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b[j], acc[i][j], 0, 0, 0);
+            }
+        }
+    }
+    wait_loads<0>(); // none may land after the workgroup's LDS is someone else's
+    constexpr int FR = GLU ? FM / 2 : FM;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        const int b = b0 + wn + 16 * j + n;
+#pragma unroll
+        for (int i = 0; i < FR; ++i) {
+            const int r = r0 + (GLU ? wm / 2 : wm) + 16 * i + 4 * quarter;
+            if (splits == 1)
+                finish4<GLU>(p, b, r, acc[i][j], acc[GLU ? i + FR : i][j]);
+            else
+                store_partial<GLU>(p, partial, b, r, acc[i][j], acc[GLU ? i + FR : i][j]);
+        }
+    }
+}
+
+// y from the splits' sums.
+template <bool GLU>
+__global__ void __launch_bounds__(256) add_splits(Operands p, const int *partial, int splits)
+{
+    const int64_t total = (int64_t)p.batch * p.rows;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        int g = 0, u = 0;
+        for (int s = 0; s < splits; ++s) {
+            g += partial[s * (GLU ? 2 : 1) * total + i];
+            if constexpr (GLU) u += partial[(2 * s + 1) * total + i];
+        }
+        const int b = (int)(i / p.rows), r = (int)(i - (int64_t)b * p.rows);
+        const float xs = p.xscale[b];
+        float v = scaled(g, xs, p.wscale[0][r]);
+        if constexpr (GLU) v = gated(v, scaled(u, xs, p.wscale[1][r]));
+        p.y[i] = half_of(v);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host.
+// ---------------------------------------------------------------------------
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+constexpr int64_t kMaxRows = (int64_t)1 << 30;
+
+bool good_sizes(int64_t rows, int64_t cols, int64_t batch)
+{
+    return rows >= 1 && rows <= kMaxRows && batch >= 1 && batch <= kMaxRows && sqllm_int8_cols(cols) > 0 &&
+           rows * batch <= (int64_t)1 << 38;
+}
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// The columns' splits of a product: `rows` of one matrix.
+int splits_of(int64_t rows, int64_t cols, int64_t batch, bool glu)
+{
+    const int64_t blocks = sqllm_int8_cols(cols) / kBlock, mine = glu ? 32 : 64;
+    const int64_t tiles = ((rows + mine - 1) / mine) * ((batch + 63) / 64);
+    int64_t s = 1;
+    while (s < 8 && tiles * s < 256 && blocks >= 16 * s) s *= 2;
+    const int64_t share = (blocks + s - 1) / s;
+    return (int)((blocks + share - 1) / share); // none empty
+}
+
+size_t workspace_bytes(int64_t rows, int64_t cols, int64_t batch, bool glu)
+{
+    if (!good_sizes(rows, cols, batch)) return 0;
+    const int splits = splits_of(rows, cols, batch, glu);
+    return up256((size_t)batch * sqllm_int8_cols(cols)) + up256((size_t)batch * 4) +
+           (splits > 1 ? (size_t)splits * batch * rows * (glu ? 8 : 4) : 0);
+}
+
+template <bool GLU, int TM, int TN, int WM, int WN, int S>
+void launch_tiled(const Operands &p, int splits, int *partial, hipStream_t stream)
+{
+    using T = Tiling<TM, TN, WM, WN, S>;
+    auto kern = gemm_tiled<GLU, TM, TN, WM, WN, S>;
+    static std::atomic<uint64_t> asked{0};
+    sqllm::dev::raise_lds_limit((const void *)kern, asked, (int)T::kLds);
+    constexpr int kRows = GLU ? TM / 2 : TM;
+    const int64_t tiles = (int64_t)((p.rows + kRows - 1) / kRows) * ((p.batch + TN - 1) / TN);
+    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(64 * T::W), T::kLds, stream, p, splits,
+                       partial);
+    if (splits > 1) {
+        const int64_t wgs = ((int64_t)p.batch * p.rows + 255) / 256;
+        hipLaunchKernelGGL(add_splits<GLU>, dim3((unsigned)std::min<int64_t>(wgs, 4096)), dim3(256), 0, stream, p, partial,
+                           splits);
+    }
+}
+
+template <bool GLU>
+sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2], int64_t rows, int64_t cols,
+                     const void *x, const float *xscale, int64_t batch, uint16_t *y, void *workspace,
+                     size_t workspace_size, hipStream_t stream)
+{
+    if (!q[0] || !scale[0] || !q[1] || !scale[1] || !x || !y) return SQLLM_ERR_NULL;
+    if (rows < 1 || rows > kMaxRows || sqllm_int8_cols(cols) == 0) return SQLLM_ERR_SHAPE;
+    if (batch < 1 || batch > kMaxRows) return SQLLM_ERR_BATCH;
+    if (!good_sizes(rows, cols, batch)) return SQLLM_ERR_SHAPE;
+    for (int k = 0; k < 2; ++k)
+        if (!aligned(q[k], 16) || !aligned(scale[k], 4)) return SQLLM_ERR_ALIGN;
+    if (!aligned(x, xscale ? 16 : 2) || !aligned(xscale, 4) || !aligned(y, 2)) return SQLLM_ERR_ALIGN;
+    if (!workspace || !aligned(workspace, 256) || workspace_size < workspace_bytes(rows, cols, batch, GLU))
+        return SQLLM_ERR_WORKSPACE;
+    const int64_t ld = sqllm_int8_cols(cols);
+    int8_t *const xq = (int8_t *)workspace;
+    float *const xs = (float *)(xq + up256((size_t)batch * ld));
+    int *const partial = (int *)((uint8_t *)xs + up256((size_t)batch * 4));
+    Operands p = {{q[0], q[1]}, {scale[0], scale[1]}, (const int8_t *)x, xscale, y, (int)rows, (int)batch, (int)(ld / kBlock)};
+    if (!xscale) {
+        if (sqllm::launch_int8_quantize((const uint16_t *)x, batch, cols, cols, xq, xs, stream) != hipSuccess)
+            return SQLLM_ERR_HIP;
+        p.xq = xq, p.xscale = xs;
+    }
+    launch_tiled<GLU, 64, 64, 32, 32, 4>(p, splits_of(rows, cols, batch, GLU), partial, stream);
+    return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
+}
+
+} // namespace
+
+extern "C" size_t sqllm_int8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
+{
+    return workspace_bytes(rows, cols, batch, false);
+}
+
+extern "C" size_t sqllm_int8_glu_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
+{
+    return workspace_bytes(rows, cols, batch, true);
+}
+
+extern "C" sqllm_status sqllm_int8_gemm(const int8_t *q, const float *scale, int64_t rows, int64_t cols, const void *x,
+                                        const float *xscale, int64_t batch, uint16_t *y, void *workspace,
+                                        size_t workspace_bytes, hipStream_t stream)
+{
+    return product<false>({q, q}, {scale, scale}, rows, cols, x, xscale, batch, y, workspace, workspace_bytes, stream);
+}
+
+extern "C" sqllm_status sqllm_int8_glu(const int8_t *gate, const float *gate_scale, const int8_t *up,
+                                       const float *up_scale, int64_t rows, int64_t cols, const void *x,
+                                       const float *xscale, int64_t batch, uint16_t *h, void *workspace,
+                                       size_t workspace_bytes, hipStream_t stream)
+{
+    return product<true>({gate, up}, {gate_scale, up_scale}, rows, cols, x, xscale, batch, h, workspace,
+                         workspace_bytes, stream);
+}

@@ -23,10 +23,12 @@ _lib.sqllm_fp8_workspace_bytes.restype = _sz
 _lib.sqllm_fp8_workspace_bytes.argtypes = [_i64, _i64, _i64]
 _lib.sqllm_fp8_gemm.restype = _i32
 _lib.sqllm_fp8_gemm.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
+_lib.sqllm_fp8_gemm_stored.restype = _i32
+_lib.sqllm_fp8_gemm_stored.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
 
 EXPORTS = ("sqllm_fp8_cols", "sqllm_fp8_scale_pitch", "sqllm_fp8_quantize", "sqllm_fp8_workspace_bytes",
-           "sqllm_fp8_gemm")
-_gemm = _lib.sqllm_fp8_gemm
+           "sqllm_fp8_gemm", "sqllm_fp8_gemm_stored")
+_gemm, _gemm_stored = _lib.sqllm_fp8_gemm, _lib.sqllm_fp8_gemm_stored
 
 
 @functools.lru_cache(maxsize=4096)
@@ -66,8 +68,9 @@ def fp8_quantize(index, handle, x: torch.Tensor, q: torch.Tensor | None = None, 
 
 @_calls.on_stream
 def fp8_gemm(index, handle, q: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: torch.Tensor | None = None,
-             ws: torch.Tensor | None = None) -> torch.Tensor:
-    """y [batch, rows] = x W^T for fp16 x [batch, cols] (or [cols]) and W stored as fp8_quantize leaves it.
+             ws: torch.Tensor | None = None, *, x_scale: torch.Tensor | None = None) -> torch.Tensor:
+    """y [batch, rows] = x W^T for fp16 x [batch, cols] (or [cols]) and W stored as fp8_quantize leaves it; with
+    x_scale, x and x_scale are in that form too (as rms_norm_fp8 leaves them).
     ws: scratch of fp8_workspace_bytes(rows, cols, batch) bytes (a cached one if None)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x: torch.Tensor expected")
@@ -78,12 +81,20 @@ def fp8_gemm(index, handle, q: torch.Tensor, scale: torch.Tensor, x: torch.Tenso
                          f"{tuple(q.shape)}")
     batch, cols = x.shape
     rows, kept = q.shape
-    if kept != fp8_cols(cols) or scale.shape != (rows, fp8_scale_pitch(cols)):
-        raise ValueError(f"q, scale: shapes {(rows, fp8_cols(cols))} and {(rows, fp8_scale_pitch(cols))} expected for "
+    pitch = fp8_scale_pitch(cols)
+    if kept != (cols if x_scale is not None else fp8_cols(cols)) or scale.shape != (rows, pitch):
+        raise ValueError(f"q, scale: shapes {(rows, fp8_cols(cols))} and {(rows, pitch)} expected for "
                          f"{cols} columns, got {tuple(q.shape)} and {tuple(scale.shape)}")
     qp, sp = _calls.address(q, "q", torch.uint8, index), _calls.address(scale, "scale", torch.uint8, index)
-    xp = _calls.address(x, "x", torch.float16, index)
+    if x_scale is not None:
+        if cols != fp8_cols(cols) or x_scale.shape != (batch, pitch):
+            raise ValueError(f"x, x_scale: shapes {(batch, fp8_cols(cols))} and {(batch, pitch)} expected, got "
+                             f"{tuple(x.shape)} and {tuple(x_scale.shape)}")
+        call, name = _gemm_stored, "sqllm_fp8_gemm_stored"
+        xs = (_calls.address(x, "x", torch.uint8, index), _calls.address(x_scale, "x_scale", torch.uint8, index))
+    else:
+        call, name, xs = _gemm, "sqllm_fp8_gemm", (_calls.address(x, "x", torch.float16, index),)
     y, yp = _calls.output(y, "y", (batch, rows), torch.float16, index)
-    _check(_calls.with_scratch(ws, fp8_workspace_bytes(rows, cols, batch), index, handle, _gemm, qp, sp, rows, cols, xp,
-                               batch, yp), "sqllm_fp8_gemm")
+    _check(_calls.with_scratch(ws, fp8_workspace_bytes(rows, cols, batch), index, handle, call, qp, sp, rows, cols, *xs,
+                               batch, yp), name)
     return y

@@ -16,6 +16,7 @@ constexpr int kBlock = 128; // columns of a stage
 using sqllm::dev::u32x2;
 using sqllm::dev::u32x4;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 // ---------------------------------------------------------------------------
 // v_mfma_i32_16x16x64_i8: lane l gives 16 bytes of row l % 16 of A (here W)
@@ -249,6 +250,118 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
     }
 }
 
+// The tiled form for large products: 256 rows (gated: 128 of each matrix) by
+// 256 rows of x in four waves of 128x128, the largest wave tile that the
+// registers hold (256 of sums): LDS is read (128 + 128) / (128 * 128) bytes for
+// each product, half of what waves of 64x64 read.  LDS is a ring of five 32 KB
+// units, W and x of a block in turn.  A block's four matrix steps (32 columns
+// each) read the fragments of the next step while they multiply, so the last
+// step of a block reads the first of the next: the barrier that says that the
+// next block is there, and that this one has been read, stands before it.  Its
+// units are loaded over from there on: x of the block after the next in that
+// step, W of the one after that in the two steps behind it.
+constexpr int kUnit = 256 * kBlock, kUnits = 5;
+
+// The swizzle here: a fragment read takes one piece of 32 rows, in two phases
+// (rows 0-3, 12-15, 20-27 and the rest); within each, row % 2 and this number
+// put the sixteen rows into the sixteen places of 16 bytes that the 64 banks
+// have.
+__device__ __forceinline__ int turn(int row) { return ((row >> 1) & 3) | ((row >> 4) & 1) << 2; }
+
+template <bool GLU>
+__global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
+{
+    constexpr int kRows = GLU ? 128 : 256, F = 4;
+    extern __shared__ __align__(16) int8_t lds[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, half = lane >> 5;
+    int r0, b0;
+    if (!tile_of<kRows, 256>(p, r0, b0)) return;
+    const uint32_t ld = (uint32_t)p.blocks * kBlock;
+    // this wave's loads of a unit: rows 64 w .. 64 w + 63 (gated: of one matrix)
+    const int8_t *const wsrc = p.wq[GLU ? w & 1 : 0] + (int64_t)r0 * ld, *const xsrc = p.xq + (int64_t)b0 * ld;
+    uint32_t wfrom[8], xfrom[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { // rows past the end: copies of the last
+        const int row = w * 64 + i * 8 + (lane >> 3), at = ((lane & 7) ^ turn(row)) * 16;
+        wfrom[i] = (uint32_t)min(GLU ? (w >> 1) * 64 + (row & 63) : row, p.rows - 1 - r0) * ld + at;
+        xfrom[i] = (uint32_t)min(row, p.batch - 1 - b0) * ld + at;
+    }
+    auto load_w = [&](int i, int k, int unit) {
+        lds_load16(wsrc + (uint32_t)min(k, p.blocks - 1) * kBlock + wfrom[i], lds + unit * kUnit + (w * 8 + i) * 1024);
+    };
+    auto load_x = [&](int i, int k, int unit) {
+        lds_load16(xsrc + (uint32_t)min(k, p.blocks - 1) * kBlock + xfrom[i], lds + unit * kUnit + (w * 8 + i) * 1024);
+    };
+    const int wm = (w & 1) * 128, wn = (w >> 1) * 128;
+    i32x16 acc[F][F];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < F; ++j) acc[i][j] = i32x16{};
+    // this lane's piece of matrix step q: 2 q + half, at its swizzled place
+    int at[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) at[q] = n * kBlock + (((2 * q + half) ^ turn(n)) * 16);
+    auto fragment = [&](int base, int q, int i) { return *(const i32x4 *)(lds + (base + at[q]) + 32 * i * kBlock); };
+    i32x4 a[2][F], b[2][F];
+    auto after = [](int u, int by) { return u + by >= kUnits ? u + by - kUnits : u + by; };
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load_w(i, k, 2 * k);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) load_x(i, k, 2 * k + 1);
+    }
+    stage_barrier<16>();
+#pragma unroll
+    for (int i = 0; i < F; ++i) {
+        a[0][i] = fragment(wm * kBlock, 0, i);
+        b[0][i] = fragment(kUnit + wn * kBlock, 0, i);
+    }
+    int unit = 0; // of W of block k; x is in the next one
+    for (int k = 0; k < p.blocks; ++k) {
+        const int next = after(unit, 2), free_w = after(unit, 4);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q == 3) stage_barrier<8>(); // all but W of block k + 2 is there, block k has been read
+            const int wbase = (q == 3 ? next : unit) * kUnit + wm * kBlock, xbase = after(q == 3 ? next : unit, 1) * kUnit + wn * kBlock;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int j = 0; j < F; j += 2) {
+                    // two matrix steps, in the first half of a step each with a
+                    // read of the next behind it, and a load, in this order
+                    const int s = i * 2 + j / 2;
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q & 1][i], b[q & 1][j], acc[i][j], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (s < F) b[(q + 1) & 1][s] = fragment(xbase, (q + 1) & 3, s);
+                    if (q == 3) load_x(s, k + 2, unit);
+                    if (q < 2 && s >= F) load_w(q * 4 + s - F, k + 2, free_w);
+                    __builtin_amdgcn_sched_barrier(0);
+                    acc[i][j + 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q & 1][i], b[q & 1][j + 1], acc[i][j + 1], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (s < F) a[(q + 1) & 1][s] = fragment(wbase, (q + 1) & 3, s);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        }
+        unit = next;
+    }
+    wait_loads<0>(); // none may land after the workgroup's LDS is someone else's
+    constexpr int FR = GLU ? F / 2 : F;
+#pragma unroll
+    for (int j = 0; j < F; ++j)
+#pragma unroll
+        for (int i = 0; i < FR; ++i)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                auto four = [&](const i32x16 &v) { return i32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]}; };
+                finish4<GLU>(p, b0 + wn + 32 * j + n, r0 + (GLU ? wm / 2 : wm) + 32 * i + 8 * g + 4 * half, four(acc[i][j]),
+                             four(acc[GLU ? i + FR : i][j]));
+            }
+}
+
 // y from the splits' sums.
 template <bool GLU>
 __global__ void __launch_bounds__(256) add_splits(Operands p, const int *partial, int splits)
@@ -322,6 +435,15 @@ void launch_tiled(const Operands &p, int splits, int *partial, hipStream_t strea
 }
 
 template <bool GLU>
+void launch_large(const Operands &p, hipStream_t stream)
+{
+    static std::atomic<uint64_t> asked{0};
+    sqllm::dev::raise_lds_limit((const void *)gemm_large<GLU>, asked, kUnits * kUnit);
+    const int64_t tiles = (int64_t)((p.rows + (GLU ? 127 : 255)) / (GLU ? 128 : 256)) * ((p.batch + 255) / 256);
+    hipLaunchKernelGGL(gemm_large<GLU>, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), kUnits * kUnit, stream, p);
+}
+
+template <bool GLU>
 sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2], int64_t rows, int64_t cols,
                      const void *x, const float *xscale, int64_t batch, uint16_t *y, void *workspace,
                      size_t workspace_size, hipStream_t stream)
@@ -345,7 +467,10 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
             return SQLLM_ERR_HIP;
         p.xq = xq, p.xscale = xs;
     }
-    launch_tiled<GLU, 64, 64, 32, 32, 4>(p, splits_of(rows, cols, batch, GLU), partial, stream);
+    if (batch > 256 && rows > 2048)
+        launch_large<GLU>(p, stream);
+    else
+        launch_tiled<GLU, 64, 64, 32, 32, 4>(p, splits_of(rows, cols, batch, GLU), partial, stream);
     return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
 }
 

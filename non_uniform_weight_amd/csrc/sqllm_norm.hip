@@ -167,13 +167,28 @@ __device__ __forceinline__ uint32_t magnitude(const float (&y)[8])
 
 constexpr uint32_t kInf = 0x7F800000u;
 
-// Eight integers nearest to y * inverse (ties to even, in one rounding): added
-// to 1.5 * 2^23, the sum's low byte is the integer.
-__device__ __forceinline__ u32x2 integers(const float (&y)[8], float inverse)
+// 127 / m in two parts, so that y * 127 / m is right to a rounding of its own:
+// fp16 values lie exactly half way between two integers now and then (m = 381,
+// y = 1.5), and with the first part alone some of them land on either side.
+struct Inverse {
+    float high, low;
+};
+
+__device__ __forceinline__ Inverse inverse_of(float m)
+{
+    const float high = 127.f / m;
+    return {high, __builtin_fmaf(-high, m, 127.f) * (high * (1.f / 127.f))};
+}
+
+// Eight integers nearest to y * inverse, ties to even: added to 1.5 * 2^23, the
+// sum's low byte is the integer.  (A value that is not half way is further from
+// it than the rounding before the sum moves it: fp16 mantissas have 11 bits.)
+__device__ __forceinline__ u32x2 integers(const float (&y)[8], Inverse inverse)
 {
     uint32_t b[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) b[k] = __float_as_uint(__builtin_fmaf(y[k], inverse, 12582912.f));
+    for (int k = 0; k < 8; ++k)
+        b[k] = __float_as_uint(__builtin_fmaf(y[k], inverse.high, y[k] * inverse.low) + 12582912.f);
     auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
         return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u),
                                      0x05040100u);
@@ -230,11 +245,11 @@ __device__ __forceinline__ void store_fp8(const Rows &a, int64_t row, int c, con
     if ((threadIdx.x & 63) == 0 && c < a.span) ((uint32_t *)a.scale)[row * a.words + (c >> 9)] = word;
 }
 
-__device__ __forceinline__ float store_scale(const Rows &a, int64_t row, uint32_t top, bool first)
+__device__ __forceinline__ Inverse store_scale(const Rows &a, int64_t row, uint32_t top, bool first)
 {
     const float m = __uint_as_float(top);
     if (first) ((float *)a.scale)[row] = top >= kInf ? NAN : m / 127.f;
-    return top == 0 || top >= kInf ? 0.f : 127.f / m;
+    return top == 0 || top >= kInf ? Inverse{0.f, 0.f} : inverse_of(m);
 }
 
 // A row in the registers of T threads, V pieces of eight values each: read
@@ -314,7 +329,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rows_kernel(Rows a)
 #pragma unroll
         for (int k = 0; k < V; ++k) top = max(top, magnitude(y[k]));
         top = row_max<T>(top, red[1]);
-        const float inverse = store_scale(a, row, top, t == 0);
+        const Inverse inverse = store_scale(a, row, top, t == 0);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int c = (k * T + t) * 8;
@@ -383,7 +398,7 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
             top = max(top, magnitude(y));
         }
         top = row_max<1024>(top, red[1]);
-        const float inverse = store_scale(a, row, top, threadIdx.x == 0);
+        const Inverse inverse = store_scale(a, row, top, threadIdx.x == 0);
         for (int c = threadIdx.x * 8; c < a.span; c += 8192) {
             value(c, y);
             *(u32x2 *)((int8_t *)a.out + row * a.ldo + c) = top >= kInf ? u32x2{0, 0} : integers(y, inverse);

@@ -316,6 +316,14 @@ def test_quantize_every_largest():
     ties[0, 1:9] = [0.5, 1.5, 2.5, 3.5, -0.5, -1.5, -2.5, 126.5]
     q, scale = nw().int8_quantize(dev(ties))
     assert scale[0] == 1 and q[0, :9].tolist() == [127, 0, 2, 2, 4, 0, -2, -2, 126]
+    for m in range(1, 9):  # steps of m / 2^k, no power of two: halves of an odd number of them are ties all the same
+        n = np.arange(0, 127)
+        x = np.append(127 * m, (n + 0.5) * m)
+        x = np.concatenate([x, -x])[None] * 2.0 ** -8
+        assert np.array_equal(x.astype(np.float16), x)
+        q, scale = nw().int8_quantize(dev(x.astype(np.float16)))
+        want = np.append(127, n + n % 2)
+        assert np.array_equal(q.cpu().numpy()[0, :256], np.concatenate([want, -want])), m
 
 
 @pytest.mark.parametrize("cols", [300, 5000, 20000, 40000])

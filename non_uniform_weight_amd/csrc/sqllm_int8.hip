@@ -13,6 +13,7 @@
 namespace {
 
 constexpr int kBlock = 128; // columns of a stage
+using sqllm::dev::f32x4;
 using sqllm::dev::u32x2;
 using sqllm::dev::u32x4;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -258,8 +259,9 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
 // each) read the fragments of the next step while they multiply, so the last
 // step of a block reads the first of the next: the barrier that says that the
 // next block is there, and that this one has been read, stands before it.  Its
-// units are loaded over from there on: x of the block after the next in that
-// step, W of the one after that in the two steps behind it.
+// units are loaded over from there on, four loads a wave and step so that none
+// waits for the others to go out: x of the block after the next in that step and
+// the one behind it, then W of the block after that.
 constexpr int kUnit = 256 * kBlock, kUnits = 5;
 
 // The swizzle here: a fragment read takes one piece of 32 rows, in two phases
@@ -294,6 +296,14 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
         lds_load16(xsrc + (uint32_t)min(k, p.blocks - 1) * kBlock + xfrom[i], lds + unit * kUnit + (w * 8 + i) * 1024);
     };
     const int wm = (w & 1) * 128, wn = (w >> 1) * 128;
+    // the scales of this wave's rows, two W rows (gated: one of each matrix) and
+    // four of x a lane
+    float ws[2], xs[F];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        ws[i] = GLU ? p.wscale[i][min(r0 + wm / 2 + lane, p.rows - 1)] : p.wscale[0][min(r0 + wm + 64 * i + lane, p.rows - 1)];
+#pragma unroll
+    for (int j = 0; j < F; ++j) xs[j] = p.xscale[min(b0 + wn + 32 * j + n, p.batch - 1)];
     i32x16 acc[F][F];
 #pragma unroll
     for (int i = 0; i < F; ++i)
@@ -311,9 +321,9 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
 #pragma unroll
         for (int i = 0; i < 8; ++i) load_w(i, k, 2 * k);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load_x(i, k, 2 * k + 1);
+        for (int i = 0; i < (k == 0 ? 8 : 4); ++i) load_x(i, k, 2 * k + 1);
     }
-    stage_barrier<16>();
+    stage_barrier<12>();
 #pragma unroll
     for (int i = 0; i < F; ++i) {
         a[0][i] = fragment(wm * kBlock, 0, i);
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
     }
     int unit = 0; // of W of block k; x is in the next one
     for (int k = 0; k < p.blocks; ++k) {
-        const int next = after(unit, 2), free_w = after(unit, 4);
+        const int next = after(unit, 2), free_x = after(unit, 3), free_w = after(unit, 4);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             if (q == 3) stage_barrier<8>(); // all but W of block k + 2 is there, block k has been read
@@ -337,8 +347,11 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q & 1][i], b[q & 1][j], acc[i][j], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
                     if (s < F) b[(q + 1) & 1][s] = fragment(xbase, (q + 1) & 3, s);
-                    if (q == 3) load_x(s, k + 2, unit);
-                    if (q < 2 && s >= F) load_w(q * 4 + s - F, k + 2, free_w);
+                    if (s % 2 == 1) {
+                        if (q == 3) load_x(s / 2, k + 2, unit);
+                        if (q == 0) load_x(4 + s / 2, k + 1, free_x);
+                        if (q == 1 || q == 2) load_w(q * 4 - 4 + s / 2, k + 2, free_w);
+                    }
                     __builtin_amdgcn_sched_barrier(0);
                     acc[i][j + 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q & 1][i], b[q & 1][j + 1], acc[i][j + 1], 0, 0, 0);
                     __builtin_amdgcn_sched_barrier(0);
@@ -348,18 +361,55 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
         }
         unit = next;
     }
-    wait_loads<0>(); // none may land after the workgroup's LDS is someone else's
-    constexpr int FR = GLU ? F / 2 : F;
+    // The sums leave through LDS: a lane holds four rows of y's columns for one of
+    // its rows, and stores of those would touch 64 lines each.  Every wave has its
+    // own 32 KB: a row of x in 2 kOut bytes, in pieces of 8 bytes at piece ^
+    // 2 (row % 16), which keeps pairs of them together.
+    constexpr int FR = GLU ? F / 2 : F, kOut = FR * 32; // columns of y of this wave
+    wait_loads<0>();
+    asm volatile("s_barrier" ::: "memory"); // the units are done with, and no load is on its way into them
+    float *const wsc = (float *)(lds + 4 * kUnit) + w * 128;
+    wsc[lane] = ws[0], wsc[64 + lane] = ws[1];
+    int8_t *const own = lds + w * kUnit;
 #pragma unroll
-    for (int j = 0; j < F; ++j)
+    for (int i = 0; i < FR; ++i)
 #pragma unroll
-        for (int i = 0; i < FR; ++i)
+        for (int g = 0; g < 4; ++g) {
+            const int r = 32 * i + 8 * g + 4 * half;
+            const f32x4 s0 = *(const f32x4 *)(wsc + r);
+            f32x4 s1 = s0;
+            if constexpr (GLU) s1 = *(const f32x4 *)(wsc + 64 + r);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                auto four = [&](const i32x16 &v) { return i32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]}; };
-                finish4<GLU>(p, b0 + wn + 32 * j + n, r0 + (GLU ? wm / 2 : wm) + 32 * i + 8 * g + 4 * half, four(acc[i][j]),
-                             four(acc[GLU ? i + FR : i][j]));
+            for (int j = 0; j < F; ++j) {
+                uint16_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = scaled(acc[i][j][4 * g + e], xs[j], s0[e]);
+                    if constexpr (GLU) v = gated(v, scaled(acc[i + FR][j][4 * g + e], xs[j], s1[e]));
+                    h[e] = half_of(v);
+                }
+                *(u32x2 *)(own + (32 * j + n) * (2 * kOut) + ((r / 4) ^ ((2 * n) & (kOut / 4 - 1) & 30)) * 8) =
+                    u32x2{h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16};
             }
+        }
+    constexpr int kLanes = kOut / 8; // of a row of x, eight columns of y each
+    const int c = lane % kLanes, r = r0 + (GLU ? wm / 2 : wm) + 8 * c;
+    const bool whole = p.rows % 8 == 0 && ((uintptr_t)p.y & 15) == 0;
+#pragma unroll 4
+    for (int k = 0; k < 128 / (64 / kLanes); ++k) {
+        const int row = k * (64 / kLanes) + lane / kLanes, b = b0 + wn + row;
+        const u32x4 v = *(const u32x4 *)(own + row * (2 * kOut) + ((2 * c) ^ ((2 * row) & (kOut / 4 - 1) & 30)) * 8);
+        if (b >= p.batch || r >= p.rows) continue;
+        uint16_t *const y = p.y + (int64_t)b * p.rows + r;
+        if (whole) {
+            *(u32x4 *)y = v;
+            continue;
+        }
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (r + e < p.rows) y[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+    }
 }
 
 // y from the splits' sums.

@@ -412,6 +412,194 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
     }
 }
 
+// Keeps a uniform address in scalar registers, so that the loads add a 32-bit
+// lane offset to it.
+typedef const __attribute__((address_space(1))) int8_t *global_ptr;
+
+__device__ __forceinline__ global_ptr scalar(const void *p)
+{
+    global_ptr g = (global_ptr)p;
+    asm("" : "+s"(g));
+    return g;
+}
+
+__device__ __forceinline__ u32x4 load_once(global_ptr base, uint32_t offset)
+{
+    return __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4 *)(base + offset));
+}
+
+// The sum over each sixteen lanes, in all of them.
+__device__ __forceinline__ int sum_of_16(int v)
+{
+#define SQLLM_ROR(n) v += __builtin_amdgcn_update_dpp(0, v, 0x120 + n, 0xF, 0xF, true)
+    SQLLM_ROR(8);
+    SQLLM_ROR(4);
+    SQLLM_ROR(2);
+    SQLLM_ROR(1);
+#undef SQLLM_ROR
+    return v;
+}
+
+// Streaming form, for few rows of x: W is read once, in whole kilobytes of a
+// row, and multiplied in the vector units (v_dot4_i32_i8, four products an
+// instruction).  A workgroup holds all of x in its registers: a chunk of 1024
+// columns is sixteen of a lane's, and the workgroup's waves share the row's
+// chunks, C of them a wave.  So it goes through groups of R rows (gated: R of
+// each matrix), chunk c of the next group on its way as soon as chunk c of this
+// one is used, and the waves' sums meet in LDS.  HALF: x comes in fp16.  Each
+// lane rounds the columns that it holds, once, while the first rows of W are on
+// their way; the largest of a row of x comes from all waves through LDS.
+constexpr int kChunk = 1024;
+
+template <bool GLU, bool HALF, int B, int C, int R>
+__global__ void __launch_bounds__(1024) gemm_dot(Operands p, const uint16_t *x, int cols, int groups)
+{
+    constexpr int M = GLU ? 2 : 1, V = (R * B + 15) / 16; // sixteens of sums of a group and matrix
+    __shared__ int part[2][16][M * V][64];
+    __shared__ uint32_t tops[B][16];
+    __shared__ float xscale[B];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+    const int ld = p.blocks * kBlock;
+    // chunks past the end: the row's last columns, with x of zero
+    uint32_t col[C];
+    bool in[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * W + w) * kChunk + lane * 16;
+        in[c] = at < ld, col[c] = min(at, ld - 16);
+    }
+    u32x4 buf[C][M][R];
+    // (live: whether there is such a group; without one every lane reads the same)
+    auto load = [&](int g, int c, bool live) {
+        const uint32_t at = live ? col[c] : 0;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                buf[c][m][r] = load_once(scalar(p.wq[m] + (int64_t)min(g * R + r, p.rows - 1) * ld), at);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    i32x4 xr[B][C];
+    if constexpr (!HALF) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const i32x4 v = *(const i32x4 *)(p.xq + (uint32_t)min(b, p.batch - 1) * (uint32_t)ld + col[c]);
+                xr[b][c] = in[c] ? v : i32x4{0, 0, 0, 0};
+            }
+        if (threadIdx.x < B) xscale[threadIdx.x] = p.xscale[min((int)threadIdx.x, p.batch - 1)];
+    }
+    int g = blockIdx.x;
+#pragma unroll
+    for (int c = 0; c < C; ++c) load(g, c, true);
+    if constexpr (HALF) {
+        u32x4 h[B][C][2];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const uint16_t *const row = x + (int64_t)min(b, p.batch - 1) * cols;
+            uint32_t top = 0;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int at = (int)col[c] + 8 * k;
+                    h[b][c][k] = in[c] && at < cols ? sqllm::rows::load8(row, at, cols) : u32x4{0, 0, 0, 0};
+                }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float y[8];
+                    sqllm::rows::floats(h[b][c][k], y);
+                    top = max(top, sqllm::rows::magnitude(y));
+                }
+            top = sqllm::rows::wave_max(top);
+            if (lane == 0) tops[b][w] = top;
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            uint32_t top = 0;
+            for (int k = 0; k < W; ++k) top = max(top, tops[b][k]);
+            const bool bad = top >= sqllm::rows::kInf;
+            const sqllm::rows::Inverse inverse = sqllm::rows::inverse_of(top);
+            if (threadIdx.x == 0) xscale[b] = sqllm::rows::scale_of(top);
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                u32x2 q[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float y[8];
+                    sqllm::rows::floats(h[b][c][k], y);
+                    q[k] = sqllm::rows::integers(y, inverse);
+                }
+                xr[b][c] = bad ? i32x4{0, 0, 0, 0} : i32x4{(int)q[0].x, (int)q[0].y, (int)q[1].x, (int)q[1].y};
+            }
+        }
+    }
+    for (int turn = 0; g < groups; g += gridDim.x, ++turn) {
+        const int next = g + gridDim.x;
+        // this lane's places: sums (lane % 16) of each sixteen, row i of the group and x row b
+        float ws[M][V];
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int m = 0; m < M; ++m) ws[m][v] = p.wscale[m][min(g * R + (16 * v + (lane & 15)) / B, p.rows - 1)];
+        int acc[M][R][B];
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int k = 0; k < B; ++k) {
+                        const i32x4 v = __builtin_bit_cast(i32x4, buf[c][m][i]);
+                        int s = c == 0 ? 0 : acc[m][i][k];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_sdot4(v[e], xr[k][c][e], s, false);
+                        asm volatile("" : "+v"(s)); // now, and not after the loads below
+                        acc[m][i][k] = s;
+                    }
+            __builtin_amdgcn_sched_barrier(0);
+            load(min(next, groups - 1), c, next < groups);
+        }
+        // sums over sixteen lanes, each of them in one of the sixteen
+        int *const mine = &part[turn & 1][w][0][lane];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                int kept = 0;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    if (16 * v + k < R * B) {
+                        const int s = sum_of_16(acc[m][(16 * v + k) / B][k % B]);
+                        kept = (lane & 15) == k ? s : kept;
+                    }
+                mine[(m * V + v) * 64] = kept;
+            }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (w != turn % W) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            int s[M];
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                s[m] = 0;
+                for (int k = 0; k < W; ++k) s[m] += part[turn & 1][k][m * V + v][lane];
+                s[m] += __shfl_xor(s[m], 16);
+                s[m] += __shfl_xor(s[m], 32);
+            }
+            const int at = 16 * v + lane, b = at % B, row = g * R + at / B;
+            float y = scaled(s[0], xscale[b], ws[0][v]);
+            if constexpr (GLU) y = gated(y, scaled(s[M - 1], xscale[b], ws[M - 1][v]));
+            if (lane < 16 && at < R * B && b < p.batch && row < p.rows) p.y[(int64_t)b * p.rows + row] = half_of(y);
+        }
+    }
+}
+
 // y from the splits' sums.
 template <bool GLU>
 __global__ void __launch_bounds__(256) add_splits(Operands p, const int *partial, int splits)
@@ -484,6 +672,51 @@ void launch_tiled(const Operands &p, int splits, int *partial, hipStream_t strea
     }
 }
 
+template <bool GLU, bool HALF, int B, int C, int R>
+void launch_dot(const Operands &p, const uint16_t *x, int cols, int waves, hipStream_t stream)
+{
+    const int groups = (p.rows + R - 1) / R;
+    int wgs = 256 * (16 / waves);
+    if (wgs > groups) wgs = groups;
+    hipLaunchKernelGGL((gemm_dot<GLU, HALF, B, C, R>), dim3(wgs), dim3(64 * waves), 0, stream, p, x, cols, groups);
+}
+
+struct Dot {
+    int waves, chunks; // of a wave; waves 0: not this form
+};
+
+Dot dot_shape(int64_t ld)
+{
+    const int total = (int)((ld + kChunk - 1) / kChunk);
+    if (total <= 8) return {total, 1};
+    if (total <= 32) return {(total + 1) / 2, 2};
+    if (total <= 48) return {(total + 2) / 3, 3};
+    return {0, 0};
+}
+
+template <bool GLU, bool HALF, int B>
+void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStream_t stream)
+{
+    constexpr int R = GLU ? 4 : 8;
+    if (d.chunks == 1)
+        launch_dot<GLU, HALF, B, 1, R>(p, x, cols, d.waves, stream);
+    else if (d.chunks == 2)
+        launch_dot<GLU, HALF, B, 2, R>(p, x, cols, d.waves, stream);
+    else
+        launch_dot<GLU, HALF, B, 3, R / 2>(p, x, cols, d.waves, stream);
+}
+
+template <bool GLU, bool HALF>
+void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStream_t stream)
+{
+    if (p.batch == 1)
+        launch_dots<GLU, HALF, 1>(p, x, cols, d, stream);
+    else if (p.batch == 2)
+        launch_dots<GLU, HALF, 2>(p, x, cols, d, stream);
+    else
+        launch_dots<GLU, HALF, 4>(p, x, cols, d, stream);
+}
+
 template <bool GLU>
 void launch_large(const Operands &p, hipStream_t stream)
 {
@@ -512,6 +745,14 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
     float *const xs = (float *)(xq + up256((size_t)batch * ld));
     int *const partial = (int *)((uint8_t *)xs + up256((size_t)batch * 4));
     Operands p = {{q[0], q[1]}, {scale[0], scale[1]}, (const int8_t *)x, xscale, y, (int)rows, (int)batch, (int)(ld / kBlock)};
+    const Dot d = batch <= 4 ? dot_shape(ld) : Dot{0, 0};
+    if (d.waves) {
+        if (xscale)
+            launch_dots<GLU, false>(p, nullptr, (int)cols, d, stream);
+        else
+            launch_dots<GLU, true>(p, (const uint16_t *)x, (int)cols, d, stream);
+        return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
+    }
     if (!xscale) {
         if (sqllm::launch_int8_quantize((const uint16_t *)x, batch, cols, cols, xq, xs, stream) != hipSuccess)
             return SQLLM_ERR_HIP;

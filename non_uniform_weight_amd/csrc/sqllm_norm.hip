@@ -14,11 +14,7 @@ namespace {
 
 using sqllm::dev::u32x2;
 using sqllm::dev::u32x4;
-// fp16 rows begin at any even address: one 16-byte access all the same (global
-// memory takes unaligned ones).
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef _Float16 half2_t __attribute__((ext_vector_type(2)));
-typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
+using namespace sqllm::rows;
 typedef short short2_t __attribute__((ext_vector_type(2)));
 
 // What is done with a row.
@@ -36,16 +32,6 @@ struct Rows {
     float eps;
 };
 
-// Eight values of a row from column c on, zeros past its end.
-__device__ __forceinline__ u32x4 load8(const uint16_t *row, int c, int cols)
-{
-    if (c + 8 <= cols) return *(const u32x4_any *)(row + c);
-    uint32_t h[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) h[k] = c + k < cols ? row[c + k] : 0;
-    return u32x4{h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-}
-
 __device__ __forceinline__ void store8(uint16_t *row, int c, int cols, u32x4 v)
 {
     if (c + 8 <= cols) {
@@ -56,36 +42,6 @@ __device__ __forceinline__ void store8(uint16_t *row, int c, int cols, u32x4 v)
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (c + k < cols) row[c + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
-}
-
-// The sum of the sixteen lanes' v and then of the wave's four sixteens, in a
-// fixed order; the largest, the same way.  In all lanes.
-#define SQLLM_ROR(v, n) __builtin_amdgcn_update_dpp(0, (int)(v), 0x120 + n, 0xF, 0xF, true)
-__device__ __forceinline__ float wave_sum(float v)
-{
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 8));
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 4));
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 2));
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 1));
-    const int b = (int)__float_as_uint(v);
-    return (__uint_as_float(__builtin_amdgcn_readlane(b, 0)) + __uint_as_float(__builtin_amdgcn_readlane(b, 16))) +
-           (__uint_as_float(__builtin_amdgcn_readlane(b, 32)) + __uint_as_float(__builtin_amdgcn_readlane(b, 48)));
-}
-
-__device__ __forceinline__ uint32_t max_of_16(uint32_t v)
-{
-    v = max(v, (uint32_t)SQLLM_ROR(v, 8));
-    v = max(v, (uint32_t)SQLLM_ROR(v, 4));
-    v = max(v, (uint32_t)SQLLM_ROR(v, 2));
-    return max(v, (uint32_t)SQLLM_ROR(v, 1));
-}
-#undef SQLLM_ROR
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t v)
-{
-    v = max_of_16(v);
-    return max(max((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
-               max((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
 }
 
 // The same over the T threads of a row; `red`: T / 64 words of LDS of its own.
@@ -156,46 +112,6 @@ __device__ __forceinline__ void normalized(u32x4 v, u32x4 w, Root root, float (&
     }
 }
 
-// Magnitudes are compared as integers: an infinity or a NaN is the largest.
-__device__ __forceinline__ uint32_t magnitude(const float (&y)[8])
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(y[k]) & 0x7FFFFFFFu);
-    return m;
-}
-
-constexpr uint32_t kInf = 0x7F800000u;
-
-// 127 / m in two parts, so that y * 127 / m is right to a rounding of its own:
-// fp16 values lie exactly half way between two integers now and then (m = 381,
-// y = 1.5), and with the first part alone some of them land on either side.
-struct Inverse {
-    float high, low;
-};
-
-__device__ __forceinline__ Inverse inverse_of(float m)
-{
-    const float high = 127.f / m;
-    return {high, __builtin_fmaf(-high, m, 127.f) * (high * (1.f / 127.f))};
-}
-
-// Eight integers nearest to y * inverse, ties to even: added to 1.5 * 2^23, the
-// sum's low byte is the integer.  (A value that is not half way is further from
-// it than the rounding before the sum moves it: fp16 mantissas have 11 bits.)
-__device__ __forceinline__ u32x2 integers(const float (&y)[8], Inverse inverse)
-{
-    uint32_t b[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        b[k] = __float_as_uint(__builtin_fmaf(y[k], inverse.high, y[k] * inverse.low) + 12582912.f);
-    auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-        return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u),
-                                     0x05040100u);
-    };
-    return u32x2{four(b[0], b[1], b[2], b[3]), four(b[4], b[5], b[6], b[7])};
-}
-
 // The e4m3 form: a block's exponent from its largest finite magnitude m * 2^p
 // (1 <= m < 2): 448 = 1.75 * 2^8, so s = p - 8, one more if m > 1.75.  Shifted
 // up by one and raised by 2^24, infinities and NaN wrap to the bottom.
@@ -247,9 +163,8 @@ __device__ __forceinline__ void store_fp8(const Rows &a, int64_t row, int c, con
 
 __device__ __forceinline__ Inverse store_scale(const Rows &a, int64_t row, uint32_t top, bool first)
 {
-    const float m = __uint_as_float(top);
-    if (first) ((float *)a.scale)[row] = top >= kInf ? NAN : m / 127.f;
-    return top == 0 || top >= kInf ? Inverse{0.f, 0.f} : inverse_of(m);
+    if (first) ((float *)a.scale)[row] = scale_of(top);
+    return inverse_of(top);
 }
 
 // A row in the registers of T threads, V pieces of eight values each: read
@@ -309,9 +224,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rows_kernel(Rows a)
     } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const half8_t h = __builtin_bit_cast(half8_t, v[k]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[k][j] = (float)h[j];
+            floats(v[k], y[k]);
         }
     }
     if constexpr (FORM == kNormHalf) {
@@ -370,9 +283,7 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
             }
         }
         if constexpr (FORM == kQuantize) {
-            const half8_t h = __builtin_bit_cast(half8_t, v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = (float)h[j];
+            floats(v, y);
         } else {
             normalized(v, c < a.cols ? load8(a.weight, c, a.cols) : u32x4{0, 0, 0, 0}, root, y);
 #pragma unroll

@@ -490,22 +490,28 @@ __global__ void __launch_bounds__(1024) gemm_dot(Operands p, const uint16_t *x, 
             }
         if (threadIdx.x < B) xscale[threadIdx.x] = p.xscale[min((int)threadIdx.x, p.batch - 1)];
     }
-    int g = blockIdx.x;
-#pragma unroll
-    for (int c = 0; c < C; ++c) load(g, c, true);
+    // (x before W, so that it is rounded while W is on its way)
+    u32x4 h[HALF ? B : 1][C][2];
     if constexpr (HALF) {
-        u32x4 h[B][C][2];
 #pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const uint16_t *const row = x + (int64_t)min(b, p.batch - 1) * cols;
-            uint32_t top = 0;
+        for (int b = 0; b < B; ++b)
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int at = (int)col[c] + 8 * k;
-                    h[b][c][k] = in[c] && at < cols ? sqllm::rows::load8(row, at, cols) : u32x4{0, 0, 0, 0};
+                    h[b][c][k] = u32x4{0, 0, 0, 0};
+                    if (in[c] && at < cols) h[b][c][k] = sqllm::rows::load8(x + (int64_t)min(b, p.batch - 1) * cols, at, cols);
                 }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    int g = blockIdx.x;
+#pragma unroll
+    for (int c = 0; c < C; ++c) load(g, c, true);
+    if constexpr (HALF) {
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            uint32_t top = 0;
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -600,6 +606,112 @@ __global__ void __launch_bounds__(1024) gemm_dot(Operands p, const uint16_t *x, 
     }
 }
 
+// Streaming form, for up to sixteen rows of x: as above on the matrix cores.
+// A workgroup holds x in its registers, S blocks of 128 columns a wave (wave w
+// those at w, w + W, ...), and goes through groups of 16 rows of W (gated: a
+// group of gate, then the same of up).  W comes through LDS, each wave with a
+// ring of D blocks of its own, loaded straight from memory, whole lines of eight
+// rows an instruction (in the matrix cores' layout it would be 64 bytes of
+// sixteen), D blocks ahead and on into the next group.
+constexpr int few_waves(int S) { return S > 8 ? 12 : 16; } // most waves of a workgroup
+
+template <bool GLU, int S, int D>
+__global__ void __launch_bounds__(64 * few_waves(S)) gemm_few(Operands p, int groups)
+{
+    static_assert(S % D == 0, "a block's place in the ring is known");
+    constexpr int M = GLU ? 2 : 1;
+    extern __shared__ __align__(16) int8_t lds[];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), W = blockDim.x >> 6;
+    const int n = lane & 15, quarter = lane >> 4;
+    int8_t *const ring = lds + w * (D * 2048);
+    i32x4 *const part = (i32x4 *)(lds + W * (D * 2048)); // [2][W][64]
+    const uint32_t ld = (uint32_t)p.blocks * kBlock;
+    // This wave's blocks, from another one on in each workgroup: where the rows
+    // are a power of two apart, the same block of all rows would lie in a few of
+    // the memory's channels.  Past the last it loads block 0, unused.
+    uint32_t at[S];
+    bool in[S];
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        const int block = ((s + blockIdx.x) % S) * W + w;
+        in[s] = block < p.blocks, at[s] = in[s] ? (uint32_t)block * kBlock : 0;
+    }
+    i32x4 x[S][2]; // on its way before W, and not waited for before it
+    const int8_t *const xrow = p.xq + (uint32_t)min(n, p.batch - 1) * ld + quarter * 16;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[s][h] = *(const i32x4 *)(xrow + at[s] + 64 * h);
+    const float xs = p.xscale[min(n, p.batch - 1)];
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    // lane l loads piece (l % 8) ^ (l / 8) of row l / 8 of eight
+    const int8_t *src[2];
+    auto rows_of = [&](int turn) { // of the turn's matrix and group
+        const int g = blockIdx.x + turn / M * gridDim.x, m = turn % M;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            src[k] = p.wq[m] + (int64_t)min(min(g, groups - 1) * 16 + 8 * k + (lane >> 3), p.rows - 1) * ld +
+                     ((lane & 7) ^ (lane >> 3)) * 16;
+    };
+    auto load = [&](int s) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) lds_load16(src[k] + at[s], ring + (s % D) * 2048 + k * 1024);
+        asm volatile("" ::: "memory"); // loads stay in this order
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    const int turns = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * M;
+    rows_of(0);
+#pragma unroll
+    for (int s = 0; s < D; ++s) load(s);
+    const int piece = n * kBlock + ((quarter ^ (n & 7)) * 16);
+    float ws[M][4] = {};
+    i32x4 gate = {0, 0, 0, 0};
+    for (int turn = 0; turn < turns; ++turn) {
+        const int g = blockIdx.x + turn / M * gridDim.x, m = turn % M;
+        // the wave that adds up this group asks for its scales before W of the next
+        const bool mine = w == turn / M % W;
+        if (mine && m == 0) {
+#pragma unroll
+            for (int k = 0; k < M; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ws[k][i] = p.wscale[k][min(g * 16 + 4 * quarter + i, p.rows - 1)];
+        }
+        i32x4 acc[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            wait_loads<2 * (D - 1)>(); // this block is there (of more loads in flight, more are)
+            asm volatile("" ::: "memory");
+            const int8_t *const b = ring + (s % D) * 2048;
+            const i32x4 lo = *(const i32x4 *)(b + piece), hi = *(const i32x4 *)(b + (piece ^ 64));
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); // read before it is loaded over
+            __builtin_amdgcn_sched_barrier(0);
+            if (s + D == S) rows_of(turn + 1); // (past the last turn the last rows again)
+            load((s + D) % S);
+            if (in[s]) {
+                acc[0] = __builtin_amdgcn_mfma_i32_16x16x64_i8(lo, x[s][0], acc[0], 0, 0, 0);
+                acc[1] = __builtin_amdgcn_mfma_i32_16x16x64_i8(hi, x[s][1], acc[1], 0, 0, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        part[((turn & 1) * W + w) * 64 + lane] = acc[0] + acc[1];
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (!mine) continue;
+        i32x4 v = {0, 0, 0, 0};
+        for (int k = 0; k < W; ++k) v += part[((turn & 1) * W + k) * 64 + lane];
+        if (m < M - 1) {
+            gate = v;
+            continue;
+        }
+        float y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = GLU ? gated(scaled(gate[i], xs, ws[0][i]), scaled(v[i], xs, ws[M - 1][i])) : scaled(v[i], xs, ws[0][i]);
+        store4(p, n, g * 16 + 4 * quarter, y);
+    }
+    wait_loads<0>(); // none may land after the workgroup's LDS is someone else's
+}
+
 // y from the splits' sums.
 template <bool GLU>
 __global__ void __launch_bounds__(256) add_splits(Operands p, const int *partial, int splits)
@@ -685,25 +797,23 @@ struct Dot {
     int waves, chunks; // of a wave; waves 0: not this form
 };
 
-Dot dot_shape(int64_t ld)
+Dot dot_shape(int64_t ld, int64_t batch)
 {
     const int total = (int)((ld + kChunk - 1) / kChunk);
+    if (batch > 4 || total > 48) return {0, 0};
     if (total <= 8) return {total, 1};
-    if (total <= 32) return {(total + 1) / 2, 2};
-    if (total <= 48) return {(total + 2) / 3, 3};
-    return {0, 0};
+    if (total <= 16) return {(total + 1) / 2, 2};
+    return {(total + 2) / 3, 3};
 }
 
 template <bool GLU, bool HALF, int B>
 void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStream_t stream)
 {
-    constexpr int R = GLU ? 4 : 8;
-    if (d.chunks == 1)
-        launch_dot<GLU, HALF, B, 1, R>(p, x, cols, d.waves, stream);
-    else if (d.chunks == 2)
-        launch_dot<GLU, HALF, B, 2, R>(p, x, cols, d.waves, stream);
-    else
-        launch_dot<GLU, HALF, B, 3, R / 2>(p, x, cols, d.waves, stream);
+    if (d.chunks == 1) launch_dot<GLU, HALF, B, 1, 4>(p, x, cols, d.waves, stream);
+    if constexpr (!HALF || B < 4)
+        if (d.chunks == 2) launch_dot<GLU, HALF, B, 2, B == 1 ? 4 : 2>(p, x, cols, d.waves, stream);
+    if constexpr (!HALF || B < 4)
+        if (d.chunks == 3) launch_dot<GLU, HALF, B, 3, 2>(p, x, cols, d.waves, stream);
 }
 
 template <bool GLU, bool HALF>
@@ -715,6 +825,16 @@ void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStrea
         launch_dots<GLU, HALF, 2>(p, x, cols, d, stream);
     else
         launch_dots<GLU, HALF, 4>(p, x, cols, d, stream);
+}
+
+template <bool GLU, int S, int D>
+void launch_few(const Operands &p, hipStream_t stream)
+{
+    static std::atomic<uint64_t> asked{0};
+    sqllm::dev::raise_lds_limit((const void *)gemm_few<GLU, S, D>, asked, 160 * 1024);
+    const int groups = (p.rows + 15) / 16, waves = (p.blocks + S - 1) / S, lds = waves * (D * 2048 + 2 * 1024);
+    const int wgs = std::min(groups, 256 * std::max(1, std::min(16 / waves, 160 * 1024 / lds)));
+    hipLaunchKernelGGL((gemm_few<GLU, S, D>), dim3(wgs), dim3(64 * waves), lds, stream, p, groups);
 }
 
 template <bool GLU>
@@ -745,12 +865,9 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
     float *const xs = (float *)(xq + up256((size_t)batch * ld));
     int *const partial = (int *)((uint8_t *)xs + up256((size_t)batch * 4));
     Operands p = {{q[0], q[1]}, {scale[0], scale[1]}, (const int8_t *)x, xscale, y, (int)rows, (int)batch, (int)(ld / kBlock)};
-    const Dot d = batch <= 4 ? dot_shape(ld) : Dot{0, 0};
-    if (d.waves) {
-        if (xscale)
-            launch_dots<GLU, false>(p, nullptr, (int)cols, d, stream);
-        else
-            launch_dots<GLU, true>(p, (const uint16_t *)x, (int)cols, d, stream);
+    const Dot d = dot_shape(ld, batch);
+    if (d.waves && !xscale && (batch <= 2 || (batch <= 4 && d.chunks == 1))) {
+        launch_dots<GLU, true>(p, (const uint16_t *)x, (int)cols, d, stream);
         return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
     }
     if (!xscale) {
@@ -758,7 +875,18 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
             return SQLLM_ERR_HIP;
         p.xq = xq, p.xscale = xs;
     }
-    if (batch > 256 && rows > 2048)
+    if (d.waves) {
+        launch_dots<GLU, false>(p, nullptr, (int)cols, d, stream);
+    } else if (batch <= 16 && p.blocks <= 192) {
+        if (p.blocks <= 32)
+            launch_few<GLU, 2, 2>(p, stream);
+        else if (p.blocks <= 64)
+            launch_few<GLU, 4, 2>(p, stream);
+        else if (p.blocks <= 128)
+            launch_few<GLU, 8, 4>(p, stream);
+        else
+            launch_few<GLU, 16, 4>(p, stream);
+    } else if (batch > 256 && rows > 2048)
         launch_large<GLU>(p, stream);
     else
         launch_tiled<GLU, 64, 64, 32, 32, 4>(p, splits_of(rows, cols, batch, GLU), partial, stream);

@@ -58,7 +58,7 @@ size_t sqllm_int8_glu_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
  *     16-byte aligned, and xscale fp32 [batch].  With xscale NULL, x is fp16,
  *     2-byte aligned, contiguous, which the call rounds to the stored form.
  *   y: fp16 [batch][rows], 2-byte aligned, must not overlap an input.
- *   1 <= rows, batch <= 2^30 (else SQLLM_ERR_SHAPE, SQLLM_ERR_BATCH) and
+ *   1 <= rows, batch <= 2^28 (else SQLLM_ERR_SHAPE, SQLLM_ERR_BATCH) and
  *   rows * batch <= 2^38 (else SQLLM_ERR_SHAPE).
  */
 sqllm_status sqllm_int8_gemm(const int8_t *q, const float *scale, int64_t rows, int64_t cols, const void *x,

@@ -84,19 +84,18 @@ __device__ __forceinline__ void finish4(const Operands &p, int b, int r, i32x4 g
     store4(p, b, r, v);
 }
 
-// The same of split blockIdx.y, as sums: partial[split][product][batch][rows].
+// The same of split blockIdx.y, as sums: partial[split][product][batch][rows
+// rounded up to four].
+__host__ __device__ __forceinline__ int64_t partial_pitch(int64_t rows) { return (rows + 3) / 4 * 4; }
+
 template <bool GLU>
 __device__ __forceinline__ void store_partial(const Operands &p, int *partial, int b, int r, i32x4 g, i32x4 u)
 {
-    if (b >= p.batch) return;
-    const int64_t size = (int64_t)p.batch * p.rows;
-    int *at = partial + blockIdx.y * (GLU ? 2 : 1) * size + (int64_t)b * p.rows + r;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (r + i < p.rows) {
-            at[i] = g[i];
-            if constexpr (GLU) at[size + i] = u[i];
-        }
+    if (b >= p.batch || r >= p.rows) return;
+    const int64_t pitch = partial_pitch(p.rows), size = p.batch * pitch;
+    int *at = partial + blockIdx.y * (GLU ? 2 : 1) * size + b * pitch + r;
+    *(i32x4 *)at = g;
+    if constexpr (GLU) *(i32x4 *)(at + size) = u;
 }
 
 // Each lane's 16 bytes at src to lds_base + 16 * lane.
@@ -128,17 +127,20 @@ __device__ __forceinline__ void stage_barrier()
 // The tile of this workgroup: its first W row and x row; false if there is
 // none.  Workgroups go round the eight XCDs: each gets a run of tiles, four W
 // tiles wide, so that the 32 it works on at once share their rows in its L2.
+// Tiles `first` to `last` (0: all of them); halves: of tiles of 2 TN rows of x.
 template <int TM, int TN>
-__device__ __forceinline__ bool tile_of(const Operands &p, int &r0, int &b0)
+__device__ __forceinline__ bool tile_of(const Operands &p, int first, int last, bool halves, int &r0, int &b0)
 {
     constexpr int G = 4;
-    const int mt = (p.rows + TM - 1) / TM, nt = (p.batch + TN - 1) / TN, tiles = mt * nt;
-    const int per = (tiles + 7) / 8, id = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || id >= tiles) return false;
+    const int wide = halves ? 2 * TN : TN;
+    const int mt = (p.rows + TM - 1) / TM, nt = (p.batch + wide - 1) / wide, mine = ((last ? last : mt * nt) - first) * (halves ? 2 : 1);
+    const int per = (mine + 7) / 8, at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    if ((int)(blockIdx.x >> 3) >= per || at >= mine) return false;
+    const int id = first + (halves ? at / 2 : at);
     const int group = id / (G * nt), in = id - group * (G * nt), width = min(G, mt - group * G);
     r0 = (group * G + in % width) * TM;
-    b0 = (in / width) * TN;
-    return true;
+    b0 = (in / width) * wide + (halves && at % 2 ? TN : 0);
+    return b0 < p.batch;
 }
 
 // Tiled form.  A workgroup computes TM rows of W (gated: TM / 2 of each matrix)
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, quarter = lane >> 4;
     int r0, b0;
-    if (!tile_of<kRows, TN>(p, r0, b0)) return;
+    if (!tile_of<kRows, TN>(p, 0, 0, false, r0, b0)) return;
     const int share = (p.blocks + splits - 1) / splits, k0 = blockIdx.y * share, k1 = min(k0 + share, p.blocks);
     if (k0 >= k1) return; // (the host leaves no split empty)
 
@@ -251,18 +253,26 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
     }
 }
 
-// The tiled form for large products: 256 rows (gated: 128 of each matrix) by
-// 256 rows of x in four waves of 128x128, the largest wave tile that the
-// registers hold (256 of sums): LDS is read (128 + 128) / (128 * 128) bytes for
-// each product, half of what waves of 64x64 read.  LDS is a ring of five 32 KB
-// units, W and x of a block in turn.  A block's four matrix steps (32 columns
-// each) read the fragments of the next step while they multiply, so the last
-// step of a block reads the first of the next: the barrier that says that the
-// next block is there, and that this one has been read, stands before it.  Its
-// units are loaded over from there on, four loads a wave and step so that none
-// waits for the others to go out: x of the block after the next in that step and
-// the one behind it, then W of the block after that.
-constexpr int kUnit = 256 * kBlock, kUnits = 5;
+// The tiled form for more rows of x: 64 FM rows (gated: half of them of each
+// matrix) by 64 FN rows of x in four waves, each 32 FM by 32 FN of them in 32x32
+// accumulators.  FM = FN = 4 is the largest wave tile that the registers hold
+// (256 of sums): LDS is read (128 + 128) / (128 * 128) bytes for each product,
+// half of what waves of 64x64 read.  LDS holds three blocks of W and two of x in
+// turn.  A block's four matrix steps (32 columns each) read the fragments of the
+// next step while they multiply, so the last step of a block reads the first of
+// the next: the barrier that says that the next block is there, and that this one
+// has been read, stands before it.  Its places are loaded over from there on, a
+// part in every step so that no load waits for others to go out: x of the block
+// after the next in that step and the one behind it, then W of the block after
+// that.  With splits > 1 a workgroup has a share of the blocks, and the sums go
+// to partial[split][product][batch][rows].
+template <int FM, int FN>
+struct Large {
+    static constexpr int kW = 64 * FM * kBlock, kX = 64 * FN * kBlock;
+    static constexpr size_t kLds = 3 * kW + 2 * kX;
+    static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+};
+constexpr int large_per_unit(int FM, int FN) { return FM * FN <= 4 ? 2 : 1; } // workgroups of a compute unit
 
 // The swizzle here: a fragment read takes one piece of 32 rows, in two phases
 // (rows 0-3, 12-15, 20-27 and the rest); within each, row % 2 and this number
@@ -270,107 +280,131 @@ constexpr int kUnit = 256 * kBlock, kUnits = 5;
 // have.
 __device__ __forceinline__ int turn(int row) { return ((row >> 1) & 3) | ((row >> 4) & 1) << 2; }
 
-template <bool GLU>
-__global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
+template <bool GLU, bool SPLIT, int FM, int FN>
+__global__ void __launch_bounds__(256, large_per_unit(FM, FN)) gemm_large(Operands p, int splits, int *partial, int first, int last, bool halves)
 {
-    constexpr int kRows = GLU ? 128 : 256, F = 4;
+    using L = Large<FM, FN>;
+    constexpr int kRows = GLU ? 32 * FM : 64 * FM; // of a matrix
     extern __shared__ __align__(16) int8_t lds[];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, half = lane >> 5;
     int r0, b0;
-    if (!tile_of<kRows, 256>(p, r0, b0)) return;
+    if (!tile_of<kRows, 64 * FN>(p, first, last, halves, r0, b0)) return;
+    const int share = SPLIT ? (p.blocks + splits - 1) / splits : p.blocks; // (the host leaves no split empty)
+    const int k0 = SPLIT ? blockIdx.y * share : 0, k1 = SPLIT ? min(k0 + share, p.blocks) : p.blocks;
     const uint32_t ld = (uint32_t)p.blocks * kBlock;
-    // this wave's loads of a unit: rows 64 w .. 64 w + 63 (gated: of one matrix)
+    // this wave's loads of a block: rows 16 FM w and on of W (gated: of one
+    // matrix), 16 FN w and on of x, eight a load.  Offsets fit 32 bits (256 rows
+    // of at most 2^17 columns).
     const int8_t *const wsrc = p.wq[GLU ? w & 1 : 0] + (int64_t)r0 * ld, *const xsrc = p.xq + (int64_t)b0 * ld;
-    uint32_t wfrom[8], xfrom[8];
+    uint32_t wfrom[2 * FM], xfrom[2 * FN];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) { // rows past the end: copies of the last
-        const int row = w * 64 + i * 8 + (lane >> 3), at = ((lane & 7) ^ turn(row)) * 16;
-        wfrom[i] = (uint32_t)min(GLU ? (w >> 1) * 64 + (row & 63) : row, p.rows - 1 - r0) * ld + at;
-        xfrom[i] = (uint32_t)min(row, p.batch - 1 - b0) * ld + at;
+    for (int i = 0; i < 2 * FM; ++i) { // rows past the end: copies of the last
+        const int row = (GLU ? w >> 1 : w) * 16 * FM + i * 8 + (lane >> 3), place = w * 16 * FM + i * 8 + (lane >> 3);
+        wfrom[i] = (uint32_t)min(row, p.rows - 1 - r0) * ld + ((lane & 7) ^ turn(place)) * 16;
     }
-    auto load_w = [&](int i, int k, int unit) {
-        lds_load16(wsrc + (uint32_t)min(k, p.blocks - 1) * kBlock + wfrom[i], lds + unit * kUnit + (w * 8 + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < 2 * FN; ++i) {
+        const int row = w * 16 * FN + i * 8 + (lane >> 3);
+        xfrom[i] = (uint32_t)min(row, p.batch - 1 - b0) * ld + ((lane & 7) ^ turn(row)) * 16;
+    }
+    int8_t *const xlds = lds + 3 * L::kW;
+    auto load_w = [&](int i, int k, int slot) {
+        lds_load16(wsrc + (uint32_t)min(k, k1 - 1) * kBlock + wfrom[i], lds + slot * L::kW + (w * 2 * FM + i) * 1024);
     };
-    auto load_x = [&](int i, int k, int unit) {
-        lds_load16(xsrc + (uint32_t)min(k, p.blocks - 1) * kBlock + xfrom[i], lds + unit * kUnit + (w * 8 + i) * 1024);
+    auto load_x = [&](int i, int k, int slot) {
+        lds_load16(xsrc + (uint32_t)min(k, k1 - 1) * kBlock + xfrom[i], xlds + slot * L::kX + (w * 2 * FN + i) * 1024);
     };
-    const int wm = (w & 1) * 128, wn = (w >> 1) * 128;
-    // the scales of this wave's rows, two W rows (gated: one of each matrix) and
-    // four of x a lane
-    float ws[2], xs[F];
+    const int wm = (w & 1) * 32 * FM, wn = (w >> 1) * 32 * FN;
+    // the scales of this wave's rows, FM / 2 W rows (gated: of both matrices) and
+    // FN of x a lane
+    float ws[FM / 2], xs[FN];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        ws[i] = GLU ? p.wscale[i][min(r0 + wm / 2 + lane, p.rows - 1)] : p.wscale[0][min(r0 + wm + 64 * i + lane, p.rows - 1)];
+    for (int i = 0; i < FM / 2; ++i) {
+        const int row = lane + 64 * i, second = GLU && row >= 16 * FM;
+        ws[i] = p.wscale[second][min(r0 + (GLU ? wm / 2 : wm) + row - second * 16 * FM, p.rows - 1)];
+    }
 #pragma unroll
-    for (int j = 0; j < F; ++j) xs[j] = p.xscale[min(b0 + wn + 32 * j + n, p.batch - 1)];
-    i32x16 acc[F][F];
+    for (int j = 0; j < FN; ++j) xs[j] = p.xscale[min(b0 + wn + 32 * j + n, p.batch - 1)];
+    i32x16 acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = i32x16{};
+        for (int j = 0; j < FN; ++j) acc[i][j] = i32x16{};
     // this lane's piece of matrix step q: 2 q + half, at its swizzled place
     int at[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) at[q] = n * kBlock + (((2 * q + half) ^ turn(n)) * 16);
-    auto fragment = [&](int base, int q, int i) { return *(const i32x4 *)(lds + (base + at[q]) + 32 * i * kBlock); };
-    i32x4 a[2][F], b[2][F];
-    auto after = [](int u, int by) { return u + by >= kUnits ? u + by - kUnits : u + by; };
+    i32x4 a[2][FM], b[2][FN];
+    // fragment r of a step: those of x first
+    auto read = [&](int to, int r, int q, int wslot, int xslot) {
+        if (r < FN)
+            b[to][r] = *(const i32x4 *)(xlds + (xslot * L::kX + wn * kBlock + at[q]) + 32 * r * kBlock);
+        else
+            a[to][r - FN] = *(const i32x4 *)(lds + (wslot * L::kW + wm * kBlock + at[q]) + 32 * (r - FN) * kBlock);
+    };
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) load_w(i, k, 2 * k);
+        for (int i = 0; i < 2 * FM; ++i) load_w(i, k0 + k, k);
 #pragma unroll
-        for (int i = 0; i < (k == 0 ? 8 : 4); ++i) load_x(i, k, 2 * k + 1);
+        for (int i = 0; i < (k == 0 ? 2 * FN : FN); ++i) load_x(i, k0 + k, k);
     }
-    stage_barrier<12>();
+    stage_barrier<2 * FM + FN>();
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        a[0][i] = fragment(wm * kBlock, 0, i);
-        b[0][i] = fragment(kUnit + wn * kBlock, 0, i);
-    }
-    int unit = 0; // of W of block k; x is in the next one
-    for (int k = 0; k < p.blocks; ++k) {
-        const int next = after(unit, 2), free_x = after(unit, 3), free_w = after(unit, 4);
+    for (int r = 0; r < FM + FN; ++r) read(0, r, 0, 0, 0);
+    int wslot = 0, xslot = 0; // of block k
+    for (int k = k0; k < k1; ++k) {
+        const int wnext = wslot == 2 ? 0 : wslot + 1, wfree = wnext == 2 ? 0 : wnext + 1;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            if (q == 3) stage_barrier<8>(); // all but W of block k + 2 is there, block k has been read
-            const int wbase = (q == 3 ? next : unit) * kUnit + wm * kBlock, xbase = after(q == 3 ? next : unit, 1) * kUnit + wn * kBlock;
+            if (q == 3) stage_barrier<2 * FM>(); // all but W of block k + 2 is there, block k has been read
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int i = 0; i < F; ++i)
-#pragma unroll
-                for (int j = 0; j < F; j += 2) {
-                    // two matrix steps, in the first half of a step each with a
-                    // read of the next behind it, and a load, in this order
-                    const int s = i * 2 + j / 2;
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q & 1][i], b[q & 1][j], acc[i][j], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (s < F) b[(q + 1) & 1][s] = fragment(xbase, (q + 1) & 3, s);
-                    if (s % 2 == 1) {
-                        if (q == 3) load_x(s / 2, k + 2, unit);
-                        if (q == 0) load_x(4 + s / 2, k + 1, free_x);
-                        if (q == 1 || q == 2) load_w(q * 4 - 4 + s / 2, k + 2, free_w);
-                    }
-                    __builtin_amdgcn_sched_barrier(0);
-                    acc[i][j + 1] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q & 1][i], b[q & 1][j + 1], acc[i][j + 1], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if (s < F) a[(q + 1) & 1][s] = fragment(wbase, (q + 1) & 3, s);
-                    __builtin_amdgcn_sched_barrier(0);
+            for (int m = 0; m < FM * FN; ++m) {
+                const int i = m / FN, j = m % FN;
+                acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a[q & 1][i], b[q & 1][j], acc[i][j], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                // a read of the next step, and a load now and then
+                if (m < FM + FN) read((q + 1) & 1, m, (q + 1) & 3, q == 3 ? wnext : wslot, q == 3 ? xslot ^ 1 : xslot);
+                if ((q & 1 ? q == 3 : q == 0) && m % FM == FM - 1) {
+                    if (q == 3)
+                        load_x(m / FM, k + 2, xslot);
+                    else
+                        load_x(FN + m / FM, k + 1, xslot ^ 1);
                 }
+                if ((q == 1 || q == 2) && m % FN == FN - 1) load_w((q - 1) * FM + m / FN, k + 2, wfree);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
-        unit = next;
+        wslot = wnext, xslot ^= 1;
+    }
+    wait_loads<0>(); // none may land after the workgroup's LDS is someone else's
+    constexpr int FR = GLU ? FM / 2 : FM, kOut = FR * 32; // columns of y of this wave
+    const int rw = r0 + (GLU ? wm / 2 : wm);
+    if constexpr (SPLIT) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int i = 0; i < FR; ++i)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    auto four = [&](const i32x16 &v) { return i32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]}; };
+                    store_partial<GLU>(p, partial, b0 + wn + 32 * j + n, rw + 32 * i + 8 * g + 4 * half, four(acc[i][j]),
+                                       four(acc[GLU ? i + FR : i][j]));
+                }
+        return;
     }
     // The sums leave through LDS: a lane holds four rows of y's columns for one of
     // its rows, and stores of those would touch 64 lines each.  Every wave has its
-    // own 32 KB: a row of x in 2 kOut bytes, in pieces of 8 bytes at piece ^
+    // own part: a row of x in 2 kOut bytes, in pieces of 8 bytes at piece ^
     // 2 (row % 16), which keeps pairs of them together.
-    constexpr int FR = GLU ? F / 2 : F, kOut = FR * 32; // columns of y of this wave
-    wait_loads<0>();
-    asm volatile("s_barrier" ::: "memory"); // the units are done with, and no load is on its way into them
-    float *const wsc = (float *)(lds + 4 * kUnit) + w * 128;
-    wsc[lane] = ws[0], wsc[64 + lane] = ws[1];
-    int8_t *const own = lds + w * kUnit;
+    asm volatile("s_barrier" ::: "memory"); // the blocks are done with, and no load is on its way into them
+    int8_t *const own = lds + w * (32 * FN * 2 * kOut);
+    float *const wsc = (float *)(lds + 4 * (32 * FN * 2 * kOut)) + w * 32 * FM;
+    static_assert(4 * 32 * FN * 2 * 32 * FM + 4 * 4 * 32 * FM <= L::kLds, "room for both");
+#pragma unroll
+    for (int i = 0; i < FM / 2; ++i) wsc[64 * i + lane] = ws[i];
 #pragma unroll
     for (int i = 0; i < FR; ++i)
 #pragma unroll
@@ -378,9 +412,9 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
             const int r = 32 * i + 8 * g + 4 * half;
             const f32x4 s0 = *(const f32x4 *)(wsc + r);
             f32x4 s1 = s0;
-            if constexpr (GLU) s1 = *(const f32x4 *)(wsc + 64 + r);
+            if constexpr (GLU) s1 = *(const f32x4 *)(wsc + 16 * FM + r);
 #pragma unroll
-            for (int j = 0; j < F; ++j) {
+            for (int j = 0; j < FN; ++j) {
                 uint16_t h[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -393,10 +427,10 @@ __global__ void __launch_bounds__(256, 1) gemm_large(Operands p)
             }
         }
     constexpr int kLanes = kOut / 8; // of a row of x, eight columns of y each
-    const int c = lane % kLanes, r = r0 + (GLU ? wm / 2 : wm) + 8 * c;
+    const int c = lane % kLanes, r = rw + 8 * c;
     const bool whole = p.rows % 8 == 0 && ((uintptr_t)p.y & 15) == 0;
 #pragma unroll 4
-    for (int k = 0; k < 128 / (64 / kLanes); ++k) {
+    for (int k = 0; k < 32 * FN * kLanes / 64; ++k) {
         const int row = k * (64 / kLanes) + lane / kLanes, b = b0 + wn + row;
         const u32x4 v = *(const u32x4 *)(own + row * (2 * kOut) + ((2 * c) ^ ((2 * row) & (kOut / 4 - 1) & 30)) * 8);
         if (b >= p.batch || r >= p.rows) continue;
@@ -712,22 +746,19 @@ __global__ void __launch_bounds__(64 * few_waves(S)) gemm_few(Operands p, int gr
     wait_loads<0>(); // none may land after the workgroup's LDS is someone else's
 }
 
-// y from the splits' sums.
+// y from the splits' sums, four rows a thread.
 template <bool GLU>
 __global__ void __launch_bounds__(256) add_splits(Operands p, const int *partial, int splits)
 {
-    const int64_t total = (int64_t)p.batch * p.rows;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        int g = 0, u = 0;
+    const int64_t pitch = partial_pitch(p.rows), size = p.batch * pitch;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < size; i += (int64_t)gridDim.x * 1024) {
+        i32x4 g = {0, 0, 0, 0}, u = {0, 0, 0, 0};
         for (int s = 0; s < splits; ++s) {
-            g += partial[s * (GLU ? 2 : 1) * total + i];
-            if constexpr (GLU) u += partial[(2 * s + 1) * total + i];
+            g += *(const i32x4 *)(partial + s * (GLU ? 2 : 1) * size + i);
+            if constexpr (GLU) u += *(const i32x4 *)(partial + (2 * s + 1) * size + i);
         }
-        const int b = (int)(i / p.rows), r = (int)(i - (int64_t)b * p.rows);
-        const float xs = p.xscale[b];
-        float v = scaled(g, xs, p.wscale[0][r]);
-        if constexpr (GLU) v = gated(v, scaled(u, xs, p.wscale[1][r]));
-        p.y[i] = half_of(v);
+        const int b = (int)(i / pitch);
+        finish4<GLU>(p, b, (int)(i - b * pitch), g, u);
     }
 }
 
@@ -737,7 +768,7 @@ __global__ void __launch_bounds__(256) add_splits(Operands p, const int *partial
 
 bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
-constexpr int64_t kMaxRows = (int64_t)1 << 30;
+constexpr int64_t kMaxRows = (int64_t)1 << 28; // the work-items of every launch fit 32 bits
 
 bool good_sizes(int64_t rows, int64_t cols, int64_t batch)
 {
@@ -747,50 +778,60 @@ bool good_sizes(int64_t rows, int64_t cols, int64_t batch)
 
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// The columns' splits of a product: `rows` of one matrix.
-int splits_of(int64_t rows, int64_t cols, int64_t batch, bool glu)
-{
-    const int64_t blocks = sqllm_int8_cols(cols) / kBlock, mine = glu ? 32 : 64;
-    const int64_t tiles = ((rows + mine - 1) / mine) * ((batch + 63) / 64);
-    int64_t s = 1;
-    while (s < 8 && tiles * s < 256 && blocks >= 16 * s) s *= 2;
-    const int64_t share = (blocks + s - 1) / s;
-    return (int)((blocks + share - 1) / share); // none empty
-}
+// Tiled forms: rows of W (gated: of both matrices) and of x, the time of a block
+// of 128 columns in us where every compute unit has one workgroup and where it
+// has two, and whether it has those at once (else one after the other).  Measured on
+// 8192x8192, 64 blocks a tile, at 256 and 512 tiles: 256x256 at batch 2048 118 us
+// and at 4096 219; 256x128 at 1024 67, at 2048 132; 128x128 at 512 45, at 1024
+// 73; 128x64 at 256 36, at 512 67; 64x64 at 128 25.5, at 256 40; 64x32 at 64
+// 22.8, at 128 31.4.
+enum Tile { k256x256, k256x128, k128x128, k128x64, k64x64, k64x32, kTiles };
+constexpr struct {
+    int tm, tn;
+    double one, two;
+    bool pairs;
+} kTile[kTiles] = {{256, 256, 1.68, 3.36, false}, {256, 128, 0.96, 1.92, false}, {128, 128, 0.66, 1.06, true},
+                   {128, 64, 0.48, 0.96, false},  {64, 64, 0.34, 0.53, true},    {64, 32, 0.29, 0.42, true}};
 
-size_t workspace_bytes(int64_t rows, int64_t cols, int64_t batch, bool glu)
-{
-    if (!good_sizes(rows, cols, batch)) return 0;
-    const int splits = splits_of(rows, cols, batch, glu);
-    return up256((size_t)batch * sqllm_int8_cols(cols)) + up256((size_t)batch * 4) +
-           (splits > 1 ? (size_t)splits * batch * rows * (glu ? 8 : 4) : 0);
-}
+// How a product is tiled: what these times make least.  Splitting the columns
+// costs a launch (5.5 us) and the sums' way through memory (4 TB/s); what is
+// left after whole rounds of 256x256 tiles goes in halves in a launch of its own
+// where that is half a round or less.  What it weighs, in us at one, two and four
+// splits: 8192x8192 at batch 17 64x32 19.6, 19.7, 17.3; at 64 128x64 34, 27, 21,
+// 64x64 26, 22, 22; at 128 64x64 25.5, 30, 32; at 256 128x64 36, 44, 55, 128x128
+// 41, 37, 40; at 512 128x128 45, 58, 73, 256x128 59, 53; 4096x4096 at 32 64x32
+// 11.6, 10.5, 10.0; at 128 64x32 11.4, 15, 18, 64x64 13.5, 13.4, 17; at 256 64x64
+// 13.6, 20, 23, 128x64 19.5, 19, 21; at 512 128x64 20.5, 29, 128x128 23, 24, 28;
+// at 1024 128x128 24.5, 37, 256x128 32, 36.
+struct Choice {
+    int tile, splits;
+    int whole; // 256x256 tiles before the halves, 0: no halves
+};
 
-template <bool GLU, int TM, int TN, int WM, int WN, int S>
-void launch_tiled(const Operands &p, int splits, int *partial, hipStream_t stream)
+Choice choose(int64_t rows, int64_t cols, int64_t batch, bool glu)
 {
-    using T = Tiling<TM, TN, WM, WN, S>;
-    auto kern = gemm_tiled<GLU, TM, TN, WM, WN, S>;
-    static std::atomic<uint64_t> asked{0};
-    sqllm::dev::raise_lds_limit((const void *)kern, asked, (int)T::kLds);
-    constexpr int kRows = GLU ? TM / 2 : TM;
-    const int64_t tiles = (int64_t)((p.rows + kRows - 1) / kRows) * ((p.batch + TN - 1) / TN);
-    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(64 * T::W), T::kLds, stream, p, splits,
-                       partial);
-    if (splits > 1) {
-        const int64_t wgs = ((int64_t)p.batch * p.rows + 255) / 256;
-        hipLaunchKernelGGL(add_splits<GLU>, dim3((unsigned)std::min<int64_t>(wgs, 4096)), dim3(256), 0, stream, p, partial,
-                           splits);
+    const int64_t blocks = sqllm_int8_cols(cols) / kBlock, m = glu ? 2 : 1;
+    Choice best = {k256x256, 1, 0};
+    double least = 1e30;
+    for (int t = 0; t < kTiles; ++t) {
+        const int64_t mine = kTile[t].tm / m, tiles = ((rows + mine - 1) / mine) * ((batch + kTile[t].tn - 1) / kTile[t].tn);
+        for (int64_t s = 1; s <= 8 && (s == 1 || (t > k256x256 && blocks >= 8 * s)); s *= 2) {
+            const int64_t share = (blocks + s - 1) / s, splits = (blocks + share - 1) / share; // none empty
+            const int64_t wgs = tiles * splits, pairs = wgs / 512, rest = wgs % 512;
+            double last = rest > 256 ? kTile[t].two : rest ? kTile[t].one : 0;
+            if (rest > 256 && kTile[t].pairs) // some units have one: the loads of the others go faster
+                last = kTile[t].one + (kTile[t].two - kTile[t].one) * (rest - 256) / 256;
+            double us = share * (pairs * kTile[t].two + last);
+            if (splits > 1) us += 5.5 + 2e-6 * splits * batch * rows * m;
+            if (us < least) least = us, best = {t, (int)splits, 0};
+            const int64_t over = wgs % 256;
+            if (t == k256x256 && wgs > 256 && over && over <= 128) {
+                us = share * (wgs / 256 * kTile[t].one + kTile[k256x128].one) + 3;
+                if (us < least) least = us, best = {t, 1, (int)(wgs - over)};
+            }
+        }
     }
-}
-
-template <bool GLU, bool HALF, int B, int C, int R>
-void launch_dot(const Operands &p, const uint16_t *x, int cols, int waves, hipStream_t stream)
-{
-    const int groups = (p.rows + R - 1) / R;
-    int wgs = 256 * (16 / waves);
-    if (wgs > groups) wgs = groups;
-    hipLaunchKernelGGL((gemm_dot<GLU, HALF, B, C, R>), dim3(wgs), dim3(64 * waves), 0, stream, p, x, cols, groups);
+    return best;
 }
 
 struct Dot {
@@ -804,6 +845,52 @@ Dot dot_shape(int64_t ld, int64_t batch)
     if (total <= 8) return {total, 1};
     if (total <= 16) return {(total + 1) / 2, 2};
     return {(total + 2) / 3, 3};
+}
+
+// Whether a streaming form takes the product.
+bool streams(int64_t cols, int64_t batch)
+{
+    const int64_t ld = sqllm_int8_cols(cols);
+    return dot_shape(ld, batch).waves || (batch <= 16 && ld <= 192 * kBlock);
+}
+
+size_t workspace_bytes(int64_t rows, int64_t cols, int64_t batch, bool glu)
+{
+    if (!good_sizes(rows, cols, batch)) return 0;
+    const int splits = streams(cols, batch) ? 1 : choose(rows, cols, batch, glu).splits;
+    return up256((size_t)batch * sqllm_int8_cols(cols)) + up256((size_t)batch * 4) +
+           (splits > 1 ? (size_t)splits * batch * partial_pitch(rows) * (glu ? 8 : 4) : 0);
+}
+
+template <bool GLU>
+void launch_add(const Operands &p, int splits, const int *partial, hipStream_t stream)
+{
+    const int64_t wgs = (p.batch * partial_pitch(p.rows) + 1023) / 1024;
+    hipLaunchKernelGGL(add_splits<GLU>, dim3((unsigned)std::min<int64_t>(wgs, 4096)), dim3(256), 0, stream, p, partial,
+                       splits);
+}
+
+template <bool GLU, int TM, int TN, int WM, int WN, int S>
+void launch_tiled(const Operands &p, int splits, int *partial, hipStream_t stream)
+{
+    using T = Tiling<TM, TN, WM, WN, S>;
+    auto kern = gemm_tiled<GLU, TM, TN, WM, WN, S>;
+    static std::atomic<uint64_t> asked{0};
+    sqllm::dev::raise_lds_limit((const void *)kern, asked, (int)T::kLds);
+    constexpr int kRows = GLU ? TM / 2 : TM;
+    const int64_t tiles = (int64_t)((p.rows + kRows - 1) / kRows) * ((p.batch + TN - 1) / TN);
+    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(64 * T::W), T::kLds, stream, p, splits,
+                       partial);
+    if (splits > 1) launch_add<GLU>(p, splits, partial, stream);
+}
+
+template <bool GLU, bool HALF, int B, int C, int R>
+void launch_dot(const Operands &p, const uint16_t *x, int cols, int waves, hipStream_t stream)
+{
+    const int groups = (p.rows + R - 1) / R;
+    int wgs = 256 * (16 / waves);
+    if (wgs > groups) wgs = groups;
+    hipLaunchKernelGGL((gemm_dot<GLU, HALF, B, C, R>), dim3(wgs), dim3(64 * waves), 0, stream, p, x, cols, groups);
 }
 
 template <bool GLU, bool HALF, int B>
@@ -837,13 +924,41 @@ void launch_few(const Operands &p, hipStream_t stream)
     hipLaunchKernelGGL((gemm_few<GLU, S, D>), dim3(wgs), dim3(64 * waves), lds, stream, p, groups);
 }
 
-template <bool GLU>
-void launch_large(const Operands &p, hipStream_t stream)
+template <bool GLU, int FM, int FN>
+void launch_large(const Operands &p, int splits, int *partial, int first, int last, bool halves, hipStream_t stream)
 {
-    static std::atomic<uint64_t> asked{0};
-    sqllm::dev::raise_lds_limit((const void *)gemm_large<GLU>, asked, kUnits * kUnit);
-    const int64_t tiles = (int64_t)((p.rows + (GLU ? 127 : 255)) / (GLU ? 128 : 256)) * ((p.batch + 255) / 256);
-    hipLaunchKernelGGL(gemm_large<GLU>, dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(256), kUnits * kUnit, stream, p);
+    using L = Large<FM, FN>;
+    auto kern = gemm_large<GLU, false, FM, FN>;
+    if constexpr (FM * FN < 16)
+        if (splits > 1) kern = gemm_large<GLU, true, FM, FN>;
+    static std::atomic<uint64_t> asked[2] = {};
+    sqllm::dev::raise_lds_limit((const void *)kern, asked[splits > 1], (int)L::kLds);
+    constexpr int kRows = GLU ? 32 * FM : 64 * FM;
+    const int wide = 64 * FN * (halves ? 2 : 1);
+    if (!last) last = ((p.rows + kRows - 1) / kRows) * ((p.batch + wide - 1) / wide);
+    const int64_t tiles = (int64_t)(last - first) * (halves ? 2 : 1);
+    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(256), L::kLds, stream, p, splits, partial,
+                       first, last, halves);
+    if (splits > 1) launch_add<GLU>(p, splits, partial, stream);
+}
+
+template <bool GLU>
+void launch_choice(const Choice &c, const Operands &p, int *partial, hipStream_t stream)
+{
+    if (c.tile == k256x256) {
+        launch_large<GLU, 4, 4>(p, 1, partial, 0, c.whole, false, stream);
+        if (c.whole) launch_large<GLU, 4, 2>(p, 1, partial, c.whole, 0, true, stream);
+    } else if (c.tile == k256x128) {
+        launch_large<GLU, 4, 2>(p, c.splits, partial, 0, 0, false, stream);
+    } else if (c.tile == k128x128) {
+        launch_large<GLU, 2, 2>(p, c.splits, partial, 0, 0, false, stream);
+    } else if (c.tile == k128x64) {
+        launch_tiled<GLU, 128, 64, 32, 64, 4>(p, c.splits, partial, stream);
+    } else if (c.tile == k64x64) {
+        launch_tiled<GLU, 64, 64, 32, 32, 4>(p, c.splits, partial, stream);
+    } else {
+        launch_tiled<GLU, 64, 32, 32, 16, 4>(p, c.splits, partial, stream);
+    }
 }
 
 template <bool GLU>
@@ -877,7 +992,7 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
     }
     if (d.waves) {
         launch_dots<GLU, false>(p, nullptr, (int)cols, d, stream);
-    } else if (batch <= 16 && p.blocks <= 192) {
+    } else if (streams(cols, batch)) {
         if (p.blocks <= 32)
             launch_few<GLU, 2, 2>(p, stream);
         else if (p.blocks <= 64)
@@ -886,10 +1001,9 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
             launch_few<GLU, 8, 4>(p, stream);
         else
             launch_few<GLU, 16, 4>(p, stream);
-    } else if (batch > 256 && rows > 2048)
-        launch_large<GLU>(p, stream);
-    else
-        launch_tiled<GLU, 64, 64, 32, 32, 4>(p, splits_of(rows, cols, batch, GLU), partial, stream);
+    } else {
+        launch_choice<GLU>(choose(rows, cols, batch, GLU), p, partial, stream);
+    }
     return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
 }
 

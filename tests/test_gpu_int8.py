@@ -69,7 +69,10 @@ SHAPES = [(1, 1, 1), (1, 16, 128), (1, 300, 4096), (2, 129, 127), (3, 64, 8320),
           (16, 2000, 16500), (16, 8200, 512), (5, 8193, 300), (3600, 3590, 130), (3400, 3841, 640), (3585, 3500, 1000),
           (500, 6100, 300), (100, 300, 16500), (40, 200, 17000), (2, 8200, 2100), (16, 8193, 2176), (9, 2050, 16400),
           (24, 2100, 5000), (90, 4100, 640), (16, 8200, 8200), (5, 700, 8300), (16, 4100, 4100), (3, 40, 131071),
-          (130, 140, 60000), (8, 30, 33000), (700, 4300, 900), (4, 4096, 4096), (2, 600, 200)]
+          (130, 140, 60000), (8, 30, 33000), (700, 4300, 900), (4, 4096, 4096), (2, 600, 200),
+          (4200, 8100, 1500), (4200, 6100, 700), (4200, 500, 300), (390, 4300, 300), (390, 2000, 300), (130, 3900, 9000),
+          (2000, 3900, 300), (130, 8100, 17000), (130, 2500, 9000), (130, 6100, 9000), (390, 1300, 9000), (390, 200, 9000),
+          (1300, 1100, 9100), (1000, 2050, 130)]
 
 
 def guarded(batch, rows):

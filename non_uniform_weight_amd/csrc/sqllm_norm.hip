@@ -44,30 +44,29 @@ __device__ __forceinline__ void store8(uint16_t *row, int c, int cols, u32x4 v)
         if (c + k < cols) row[c + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
 }
 
-// The same over the T threads of a row; `red`: T / 64 words of LDS of its own.
-template <int T>
+// The same over a row's threads.  ONE: they are a wave; else the workgroup, of
+// up to sixteen, and `red` is sixteen words of LDS of its own.
+template <bool ONE>
 __device__ __forceinline__ float row_sum(float v, uint32_t *red)
 {
     v = wave_sum(v);
-    if constexpr (T > 64) {
+    if constexpr (!ONE) {
         red[threadIdx.x >> 6] = __float_as_uint(v);
         __syncthreads();
         v = 0.f;
-#pragma unroll
-        for (int k = 0; k < T / 64; ++k) v += __uint_as_float(red[k]);
+        for (uint32_t k = 0; k < blockDim.x >> 6; ++k) v += __uint_as_float(red[k]);
     }
     return v;
 }
 
-template <int T>
+template <bool ONE>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *red)
 {
     v = wave_max(v);
-    if constexpr (T > 64) {
+    if constexpr (!ONE) {
         red[threadIdx.x >> 6] = v;
         __syncthreads();
-#pragma unroll
-        for (int k = 0; k < T / 64; ++k) v = max(v, red[k]);
+        for (uint32_t k = 0; k < blockDim.x >> 6; ++k) v = max(v, red[k]);
     }
     return v;
 }
@@ -167,44 +166,34 @@ __device__ __forceinline__ Inverse store_scale(const Rows &a, int64_t row, uint3
     return inverse_of(top);
 }
 
-// A row in the registers of T threads, V pieces of eight values each: read
-// once, written once.  Rows of 64 threads: four a workgroup, no barrier.
-template <int FORM, bool RES, int T, int V>
-__global__ void __launch_bounds__(T < 256 ? 256 : T) rows_kernel(Rows a)
+// A row in the registers of a wave (ONE; four rows a workgroup, no barrier) or
+// of a workgroup, V pieces of eight values a thread: read once, written once.
+template <int FORM, bool RES, bool ONE, int V>
+__global__ void __launch_bounds__(ONE ? 256 : 1024) rows_kernel(Rows a)
 {
-    constexpr int W = T / 64;
-    __shared__ uint32_t red[2][W];
-    const int t = threadIdx.x % T;
-    const int64_t row = T < 256 ? (int64_t)blockIdx.x * (256 / T) + __builtin_amdgcn_readfirstlane(threadIdx.x / T) : blockIdx.x;
-    static_assert(T == 64 || T >= 256, "a row of fewer than 256 threads is one wave's: it leaves before no barrier");
-    if (row >= a.rows) return;
+    __shared__ uint32_t red[2][16];
+    const int T = ONE ? 64 : blockDim.x, t = ONE ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t row = ONE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
+    if (ONE && row >= a.rows) return;
     const uint16_t *const x = a.x + row * a.ldx;
-    u32x4 v[V], w[FORM == kQuantize ? 1 : V];
+    u32x4 v[V], r[RES ? V : 1], w[FORM == kQuantize ? 1 : V];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int c = (k * T + t) * 8;
         v[k] = u32x4{0, 0, 0, 0};
-        if (c < a.cols) v[k] = load8(x, c, a.cols);
-    }
-    if constexpr (RES) {
-        u32x4 r[V];
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = (k * T + t) * 8;
-            r[k] = u32x4{0, 0, 0, 0};
-            if (c < a.cols) r[k] = load8(a.residual + row * a.ldr, c, a.cols);
+        if constexpr (RES) r[k] = v[k];
+        if constexpr (FORM != kQuantize) w[k] = v[k];
+        if (c < a.cols) {
+            v[k] = load8(x, c, a.cols);
+            if constexpr (RES) r[k] = load8(a.residual + row * a.ldr, c, a.cols);
+            if constexpr (FORM != kQuantize) w[k] = load8(a.weight, c, a.cols);
         }
+    }
+    if constexpr (RES)
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = add8(v[k], r[k]);
-    }
     float y[V][8];
     if constexpr (FORM != kQuantize) {
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int c = (k * T + t) * 8;
-            w[k] = u32x4{0, 0, 0, 0};
-            if (c < a.cols) w[k] = load8(a.weight, c, a.cols);
-        }
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -212,7 +201,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rows_kernel(Rows a)
             if (RES && a.sum && c < a.cols) store8(a.sum + row * a.cols, c, a.cols, v[k]);
             s += squares(v[k], 0.f);
         }
-        const Root root = reciprocal_root(row_sum<T>(s, red[0]) / (float)a.cols + a.eps);
+        const Root root = reciprocal_root(row_sum<ONE>(s, red[0]) / (float)a.cols + a.eps);
 #pragma unroll
         for (int k = 0; k < V; ++k) normalized(v[k], w[k], root, y[k]);
         // (a root of infinity or NaN turns the zeros past the end into NaN)
@@ -241,7 +230,7 @@ __global__ void __launch_bounds__(T < 256 ? 256 : T) rows_kernel(Rows a)
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) top = max(top, magnitude(y[k]));
-        top = row_max<T>(top, red[1]);
+        top = row_max<ONE>(top, red[1]);
         const Inverse inverse = store_scale(a, row, top, t == 0);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -270,7 +259,7 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
             }
             s += squares(v, 0.f);
         }
-        root = reciprocal_root(row_sum<1024>(s, red[0]) / (float)a.cols + a.eps);
+        root = reciprocal_root(row_sum<false>(s, red[0]) / (float)a.cols + a.eps);
     }
     auto value = [&](int c, float (&y)[8]) {
         u32x4 v = u32x4{0, 0, 0, 0};
@@ -308,7 +297,7 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
             value(c, y);
             top = max(top, magnitude(y));
         }
-        top = row_max<1024>(top, red[1]);
+        top = row_max<false>(top, red[1]);
         const Inverse inverse = store_scale(a, row, top, threadIdx.x == 0);
         for (int c = threadIdx.x * 8; c < a.span; c += 8192) {
             value(c, y);
@@ -321,16 +310,35 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
 // Host.
 // ---------------------------------------------------------------------------
 
+// Threads of a row: as many as leave one piece each up to 512, two up to 1024
+// threads, more beyond; shorter rows are a wave's.  us at one, two, three and
+// four pieces a thread (with the residual, fp16 out): 1x4096 2.6, 2.9, 3.5, 4.0;
+// 16x8192 3.3, 3.2, 3.9, 4.5; 4096x4096 23.2, 23.1, 25.2, 26.2; 4096x8192 44, 42,
+// 45, 47 (6.4 TB/s); 1000x24576 at three 39, at four 41 (without a residual 20.4
+// and 26).  The quantiser holds less, and where rows are many has room for four:
+// 4096x4096 at two and four 11.0 and 10.4, 1024x16384 11.5 and 10.3, 4096x8192
+// 18.1 and 17.8 (5.7 TB/s), but 300x5120 3.6 and 3.8, 4096x1024 4.5 at one, 5.3.
 template <int FORM, bool RES>
 hipError_t launch_rows(const Rows &a, hipStream_t stream)
 {
     const int pieces = (a.span + 7) / 8;
-    if (pieces <= 128)
-        hipLaunchKernelGGL((rows_kernel<FORM, RES, 64, 2>), dim3((a.rows + 3) / 4), dim3(256), 0, stream, a);
-    else if (pieces <= 1024)
-        hipLaunchKernelGGL((rows_kernel<FORM, RES, 256, 4>), dim3(a.rows), dim3(256), 0, stream, a);
-    else if (pieces <= 4096)
-        hipLaunchKernelGGL((rows_kernel<FORM, RES, 1024, 4>), dim3(a.rows), dim3(1024), 0, stream, a);
+    auto launch = [&](auto kern, int v) {
+        hipLaunchKernelGGL(kern, dim3(a.rows), dim3((pieces + 64 * v - 1) / (64 * v) * 64), 0, stream, a);
+    };
+    if (pieces <= 64)
+        hipLaunchKernelGGL((rows_kernel<FORM, RES, true, 1>), dim3((a.rows + 3) / 4), dim3(256), 0, stream, a);
+    else if (pieces <= 128)
+        hipLaunchKernelGGL((rows_kernel<FORM, RES, true, 2>), dim3((a.rows + 3) / 4), dim3(256), 0, stream, a);
+    else if (FORM == kQuantize && a.rows >= 1000 && pieces > 256 && pieces <= 4096)
+        launch(rows_kernel<FORM, RES, false, 4>, 4);
+    else if (pieces <= 512)
+        launch(rows_kernel<FORM, RES, false, 1>, 1);
+    else if (pieces <= 2 * 1024)
+        launch(rows_kernel<FORM, RES, false, 2>, 2);
+    else if (pieces <= 3 * 1024)
+        launch(rows_kernel<FORM, RES, false, 3>, 3);
+    else if (pieces <= 4 * 1024)
+        launch(rows_kernel<FORM, RES, false, 4>, 4);
     else
         hipLaunchKernelGGL((long_rows_kernel<FORM, RES>), dim3(a.rows), dim3(1024), 0, stream, a);
     return hipGetLastError();

@@ -117,7 +117,7 @@ def call(form):
 
 
 SHAPES = [(1, 1), (1, 7), (3, 8), (5, 127), (2, 128), (7, 129), (1, 513), (33, 1000), (6, 1024), (5, 1025), (9, 2049),
-          (4, 4096), (130, 5001), (2, 8192), (3, 8200), (2, 16385), (1, 32768), (2, 32769), (1, 40003), (300, 64)]
+          (4, 4096), (130, 5001), (2, 8192), (3, 8200), (2, 16385), (1, 32768), (2, 32769), (1, 40003), (300, 64), (2, 16500), (2, 24600), (1100, 2600)]
 
 
 @pytest.mark.parametrize("form", ["fp16", "int8", "fp8"])

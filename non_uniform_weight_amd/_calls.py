@@ -61,13 +61,12 @@ def half_rows(x, name: str, index: int):
     """(rows, columns, values from a row to the next, address) of fp16 x [rows, cols], its columns adjacent."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: torch.Tensor expected")
-    if x.dim() != 2 or x.numel() == 0:
-        raise ValueError(f"{name}: shape (rows, cols) expected, got {tuple(x.shape)}")
-    if x.get_device() != index:
-        raise ValueError(f"{name}: on {x.device}, the call's other tensors on cuda:{index}")
-    if x.dtype is not torch.float16:
-        raise TypeError(f"{name}: dtype torch.float16 expected, got {x.dtype}")
-    rows, cols = x.shape
+    shape = x.shape
+    if len(shape) != 2 or 0 in shape:
+        raise ValueError(f"{name}: shape (rows, cols) expected, got {tuple(shape)}")
+    if x.dtype is not torch.float16 or x.get_device() != index:
+        _checked_address(x, name, torch.float16, index)
+    rows, cols = shape
     if x.is_contiguous():
         return rows, cols, cols, x.data_ptr()
     if cols > 1 and x.stride(1) != 1:

@@ -73,16 +73,17 @@ def _activations(x, x_scale, kept, index):
     stored, cols = cols, min(cols, _MAX_COLS)  # (the longest rows' last stored column is padding)
     if stored != kept or kept != int8_cols(cols):
         raise ValueError(f"x: the weights' {kept} stored columns (a multiple of 128) expected, got {stored}")
+    xp, xsp = _calls.address(x, "x", torch.int8, index), _calls.address(x_scale, "x_scale", torch.float32, index)
     if x_scale.numel() != batch:
         raise ValueError(f"x_scale: {batch} values expected, got {x_scale.numel()}")
-    return (batch, cols, _calls.address(x, "x", torch.int8, index),
-            _calls.address(x_scale, "x_scale", torch.float32, index))
+    return batch, cols, xp, xsp
 
 
 def _weights(q, scale, name, index):
-    if q.dim() != 2 or scale.shape != (q.shape[0],):
+    qp, sp = _calls.address(q, name, torch.int8, index), _calls.address(scale, f"{name}'s scale", torch.float32, index)
+    if q.dim() != 2 or scale.shape != q.shape[:1]:
         raise ValueError(f"{name}: shapes (rows, columns) and (rows,) expected, got {tuple(q.shape)}, {tuple(scale.shape)}")
-    return _calls.address(q, name, torch.int8, index), _calls.address(scale, f"{name}'s scale", torch.float32, index)
+    return qp, sp
 
 
 @_calls.on_stream

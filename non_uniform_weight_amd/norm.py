@@ -24,6 +24,14 @@ EXPORTS = ("sqllm_rms_norm", "sqllm_rms_norm_int8", "sqllm_rms_norm_fp8")
 _half, _int8, _fp8 = _lib.sqllm_rms_norm, _lib.sqllm_rms_norm_int8, _lib.sqllm_rms_norm_fp8
 
 
+def _half_output(t, name, x, rows, cols, index):
+    """As _calls.output, for one that is like x."""
+    if t is None and x.is_contiguous():  # half a microsecond less than by shape, type and device
+        t = torch.empty_like(x)
+        return t, t.data_ptr()
+    return _calls.output(t, name, (rows, cols), torch.float16, index)
+
+
 def _inputs(x, weight, eps, residual, total, index):
     """(rows, cols, the C calls' arguments up to sum, sum); sum as a tuple of none or one."""
     rows, cols, ldx, xp = _calls.half_rows(x, "x", index)
@@ -37,7 +45,7 @@ def _inputs(x, weight, eps, residual, total, index):
     if residual.shape != x.shape:
         raise ValueError(f"residual: shape {tuple(x.shape)} expected, got {tuple(residual.shape)}")
     _, _, ldr, rp = _calls.half_rows(residual, "residual", index)
-    total, tp = _calls.output(total, "total", (rows, cols), torch.float16, index)
+    total, tp = _half_output(total, "total", x, rows, cols, index)
     return rows, cols, (xp, ldx, rp, ldr, wp, rows, cols, eps, tp), (total,)
 
 
@@ -48,7 +56,7 @@ def rms_norm(index, handle, x: torch.Tensor, weight: torch.Tensor, eps: float, r
     (y, total): the norm of total = x + residual.  total may be x or residual itself; the rows of x and residual may
     be further apart than cols.  stream: as for every call (keyword)."""
     rows, cols, args, total = _inputs(x, weight, eps, residual, total, index)
-    y, yp = _calls.output(y, "y", (rows, cols), torch.float16, index)
+    y, yp = _half_output(y, "y", x, rows, cols, index)
     _check(_half(*args, yp, handle), "sqllm_rms_norm")
     return (y, *total) if total else y
 

@@ -311,3 +311,59 @@ def test_fp8_gemm_of_stored_activations(batch, rows, cols):
     tol = cols * 2.0 ** -23 * mag + 7 * 2.0 ** -13 * cut + 2.0 ** -11 * ref.abs() + 2.0 ** -25
     assert ((y.double() - ref).abs() <= tol).all()
     assert (guard[:256] == 7).all() and (guard[256 + batch * rows:] == 7).all()
+
+
+# ------------------------------------------------------------------------------------------- beyond 32-bit offsets
+@pytest.mark.parametrize("batch", [1, 3, 16, 40, 300])
+def test_weights_past_four_gigabytes(batch):
+    """The last rows of a matrix whose codes lie past 2^32 bytes."""
+    step(f"int8 weights past 4 GB, batch {batch}")
+    rows, cols = 200003, 24000  # 24064 stored columns: 4.8 GB
+    q, scale = codes(rows, cols, 3)
+    x = acts(batch, cols, 5)
+    xq, xs = nw().int8_quantize(x)
+    at = torch.arange(rows - 77, rows, device="cuda")
+    want = number(q[at], scale[at], xq, xs)
+    for y in (nw().int8_gemm(q, scale, xq, xs), nw().int8_gemm(q, scale, x)):
+        same(y[:, at], want)
+        same(y[:, :50], number(q[:50], scale[:50], xq, xs))
+    # gate from the front of the same memory, up from its end: both matrices of 178 000 rows
+    n = 178000
+    g, u, first = q[:n], q[rows - n:], torch.arange(n - 60, n, device="cuda")
+    h = nw().int8_glu(g, scale[:n], u, scale[rows - n:], xq, xs)
+    check_glu(h[:, first], number(g[first], scale[first], xq, xs), number(u[first], scale[rows - n:][first], xq, xs))
+
+
+def test_results_past_four_gigabytes():
+    step("int8 results past 4 GB")
+    batch, rows, cols = 70000, 33000, 128
+    q, scale = codes(rows, cols, 3)
+    xq, xs = nw().int8_quantize(acts(batch, cols, 5))
+    y = nw().int8_gemm(q, scale, xq, xs)
+    b, r = torch.tensor([0, 1, 35000, batch - 2, batch - 1], device="cuda"), torch.arange(rows - 300, rows, device="cuda")
+    same(y[b][:, r], number(q[r], scale[r], xq[b], xs[b]))
+    del y
+    h = nw().int8_glu(q, scale, q, scale, xq, xs)
+    check_glu(h[b][:, r], *[number(q[r], scale[r], xq[b], xs[b])] * 2)
+
+
+def test_first_calls_inside_a_capture():
+    """Shapes that no call before took (each launch's one-time settings are made there), captured at once."""
+    step("int8 captured first")
+    made = []
+    for batch, rows, cols in ((6, 900, 17000), (77, 900, 9000), (900, 6000, 200), (300, 2000, 300)):
+        q, scale = codes(rows, cols, batch)
+        xq, xs = nw().int8_quantize(acts(batch, cols, 2))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = nw().int8_gemm(q, scale, xq, xs)
+            h = nw().int8_glu(q, scale, q, scale, xq, xs)
+        made.append((g, y, h, number(q, scale, xq, xs), (q, scale, xq, xs)))  # a graph's inputs live as long as it
+    for _ in range(3):
+        for g, y, h, *_ in made:
+            y.fill_(1), h.fill_(1)
+            g.replay()
+        torch.cuda.synchronize()
+        for _, y, h, want, _ in made:
+            same(y, want)
+            check_glu(h, want, want)

@@ -342,3 +342,22 @@ def test_quantize_strided_rows(offset, width):
     full = rows_of(9, width, offset)
     q, scale = nw().int8_quantize(dev(full)[:, offset:offset + 500])
     check_int8(q, scale, full[:, offset:offset + 500].astype(np.float64), 2.0 ** -24, 127 * 2.0 ** -24)
+
+
+def test_rows_past_four_gigabytes():
+    """The last rows of activations that lie past 2^32 bytes, inputs and outputs."""
+    step("norm past 4 GB")
+    rows, cols = 290001, 8000  # 4.6 GB
+    x = torch.empty(rows, cols, dtype=torch.float16, device="cuda")
+    for part in x.split(20000):
+        part.normal_(generator=torch.Generator(device="cuda").manual_seed(part.shape[0]))
+    w = dev(weight_of(cols, 2))
+    at = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1], device="cuda")
+    xh = x[at].cpu().numpy()
+    ref, total = reference(xh, w.cpu().numpy(), res=xh)
+    for form in ("fp16", "int8", "fp8"):
+        got = call(form)(x, w, EPS, residual=x)
+        check(form, tuple(t[at] for t in got), ref, total, e_of(cols))
+        del got
+    q, scale = nw().int8_quantize(x)
+    check_int8(q[at], scale[at], xh.astype(np.float64), 2.0 ** -24, 127 * 2.0 ** -24)

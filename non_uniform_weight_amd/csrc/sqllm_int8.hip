@@ -46,9 +46,10 @@ __device__ __forceinline__ uint16_t half_of(float v)
     return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// A sum as a number; silu(g) u.
+// A sum as a number; silu(g) u, the quotient by the hardware's reciprocal (a
+// step of 2^-23; a division takes ten instructions, 1.5 us of a 256x256 tile).
 __device__ __forceinline__ float scaled(int sum, float xs, float ws) { return (float)sum * (xs * ws); }
-__device__ __forceinline__ float gated(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+__device__ __forceinline__ float gated(float g, float u) { return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u; }
 
 // Four W rows r..r+3 of one x row, rounded once; in one store where the row of
 // y is aligned for it.

@@ -130,13 +130,13 @@ __device__ __forceinline__ void stage_barrier()
 // tiles wide, so that the 32 it works on at once share their rows in its L2.
 // Tiles `first` to `last` (0: all of them); halves: of tiles of 2 TN rows of x.
 template <int TM, int TN>
-__device__ __forceinline__ bool tile_of(const Operands &p, int first, int last, bool halves, int &r0, int &b0)
+__device__ __forceinline__ bool tile_of(const Operands &p, int wg, int first, int last, bool halves, int &r0, int &b0)
 {
     constexpr int G = 4;
     const int wide = halves ? 2 * TN : TN;
     const int mt = (p.rows + TM - 1) / TM, nt = (p.batch + wide - 1) / wide, mine = ((last ? last : mt * nt) - first) * (halves ? 2 : 1);
-    const int per = (mine + 7) / 8, at = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if ((int)(blockIdx.x >> 3) >= per || at >= mine) return false;
+    const int per = (mine + 7) / 8, at = (wg & 7) * per + (wg >> 3);
+    if (wg >> 3 >= per || at >= mine) return false;
     const int id = first + (halves ? at / 2 : at);
     const int group = id / (G * nt), in = id - group * (G * nt), width = min(G, mt - group * G);
     r0 = (group * G + in % width) * TM;
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, quarter = lane >> 4;
     int r0, b0;
-    if (!tile_of<kRows, TN>(p, 0, 0, false, r0, b0)) return;
+    if (!tile_of<kRows, TN>(p, blockIdx.x, 0, 0, false, r0, b0)) return;
     const int share = (p.blocks + splits - 1) / splits, k0 = blockIdx.y * share, k1 = min(k0 + share, p.blocks);
     if (k0 >= k1) return; // (the host leaves no split empty)
 
@@ -282,15 +282,12 @@ constexpr int large_per_unit(int FM, int FN) { return FM * FN <= 4 ? 2 : 1; } //
 __device__ __forceinline__ int turn(int row) { return ((row >> 1) & 3) | ((row >> 4) & 1) << 2; }
 
 template <bool GLU, bool SPLIT, int FM, int FN>
-__global__ void __launch_bounds__(256, large_per_unit(FM, FN)) gemm_large(Operands p, int splits, int *partial, int first, int last, bool halves)
+__device__ __forceinline__ void large_tile(const Operands &p, int splits, int *partial, int r0, int b0)
 {
     using L = Large<FM, FN>;
-    constexpr int kRows = GLU ? 32 * FM : 64 * FM; // of a matrix
     extern __shared__ __align__(16) int8_t lds[];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, half = lane >> 5;
-    int r0, b0;
-    if (!tile_of<kRows, 64 * FN>(p, first, last, halves, r0, b0)) return;
     const int share = SPLIT ? (p.blocks + splits - 1) / splits : p.blocks; // (the host leaves no split empty)
     const int k0 = SPLIT ? blockIdx.y * share : 0, k1 = SPLIT ? min(k0 + share, p.blocks) : p.blocks;
     const uint32_t ld = (uint32_t)p.blocks * kBlock;
@@ -444,6 +441,28 @@ __global__ void __launch_bounds__(256, large_per_unit(FM, FN)) gemm_large(Operan
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (r + e < p.rows) y[e] = (uint16_t)(u[e >> 1] >> (16 * (e & 1)));
+    }
+}
+
+template <bool GLU, bool SPLIT, int FM, int FN>
+__global__ void __launch_bounds__(256, large_per_unit(FM, FN)) gemm_large(Operands p, int splits, int *partial)
+{
+    int r0, b0;
+    if (tile_of<GLU ? 32 * FM : 64 * FM, 64 * FN>(p, blockIdx.x, 0, 0, false, r0, b0))
+        large_tile<GLU, SPLIT, FM, FN>(p, splits, partial, r0, b0);
+}
+
+// Whole rounds of 256x256 tiles, and what is left of them in halves: those begin
+// on each compute unit as soon as it is done with its last whole one.
+template <bool GLU>
+__global__ void __launch_bounds__(256, 1) gemm_large_halves(Operands p, int whole)
+{
+    constexpr int kRows = GLU ? 128 : 256;
+    int r0, b0;
+    if ((int)blockIdx.x < whole) {
+        if (tile_of<kRows, 256>(p, blockIdx.x, 0, whole, false, r0, b0)) large_tile<GLU, false, 4, 4>(p, 1, nullptr, r0, b0);
+    } else {
+        if (tile_of<kRows, 128>(p, blockIdx.x - whole, whole, 0, true, r0, b0)) large_tile<GLU, false, 4, 2>(p, 1, nullptr, r0, b0);
     }
 }
 
@@ -796,8 +815,9 @@ constexpr struct {
 
 // How a product is tiled: what these times make least.  Splitting the columns
 // costs a launch (5.5 us) and the sums' way through memory (4 TB/s); what is
-// left after whole rounds of 256x256 tiles goes in halves in a launch of its own
-// where that is half a round or less.  What it weighs, in us at one, two and four
+// left after whole rounds of 256x256 tiles goes in halves where that is half a
+// round or less (gated 13824x5120 at batch 2048, 864 tiles: 262 us, 275 without;
+// 5120x5120 at 8192, 640: 188 and 200).  What it weighs, in us at one, two and four
 // splits: 8192x8192 at batch 17 64x32 19.6, 19.7, 17.3; at 64 128x64 34, 27, 21,
 // 64x64 26, 22, 22; at 128 64x64 25.5, 30, 32; at 256 128x64 36, 44, 55, 128x128
 // 41, 37, 40; at 512 128x128 45, 58, 73, 256x128 59, 53; 4096x4096 at 32 64x32
@@ -827,7 +847,7 @@ Choice choose(int64_t rows, int64_t cols, int64_t batch, bool glu)
             if (us < least) least = us, best = {t, (int)splits, 0};
             const int64_t over = wgs % 256;
             if (t == k256x256 && wgs > 256 && over && over <= 128) {
-                us = share * (wgs / 256 * kTile[t].one + kTile[k256x128].one) + 3;
+                us = share * (wgs / 256 * kTile[t].one + kTile[k256x128].one);
                 if (us < least) least = us, best = {t, 1, (int)(wgs - over)};
             }
         }
@@ -926,7 +946,7 @@ void launch_few(const Operands &p, hipStream_t stream)
 }
 
 template <bool GLU, int FM, int FN>
-void launch_large(const Operands &p, int splits, int *partial, int first, int last, bool halves, hipStream_t stream)
+void launch_large(const Operands &p, int splits, int *partial, hipStream_t stream)
 {
     using L = Large<FM, FN>;
     auto kern = gemm_large<GLU, false, FM, FN>;
@@ -935,24 +955,33 @@ void launch_large(const Operands &p, int splits, int *partial, int first, int la
     static std::atomic<uint64_t> asked[2] = {};
     sqllm::dev::raise_lds_limit((const void *)kern, asked[splits > 1], (int)L::kLds);
     constexpr int kRows = GLU ? 32 * FM : 64 * FM;
-    const int wide = 64 * FN * (halves ? 2 : 1);
-    if (!last) last = ((p.rows + kRows - 1) / kRows) * ((p.batch + wide - 1) / wide);
-    const int64_t tiles = (int64_t)(last - first) * (halves ? 2 : 1);
-    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(256), L::kLds, stream, p, splits, partial,
-                       first, last, halves);
+    const int64_t tiles = (int64_t)((p.rows + kRows - 1) / kRows) * ((p.batch + 64 * FN - 1) / (64 * FN));
+    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(256), L::kLds, stream, p, splits, partial);
     if (splits > 1) launch_add<GLU>(p, splits, partial, stream);
+}
+
+template <bool GLU>
+void launch_halves(const Operands &p, int whole, hipStream_t stream)
+{
+    static std::atomic<uint64_t> asked{0};
+    constexpr int kLds = Large<4, 4>::kLds, kRows = GLU ? 128 : 256;
+    sqllm::dev::raise_lds_limit((const void *)gemm_large_halves<GLU>, asked, kLds);
+    const int64_t tiles = (int64_t)((p.rows + kRows - 1) / kRows) * ((p.batch + 255) / 256);
+    const int64_t wgs = whole + ((tiles - whole) * 2 + 7) / 8 * 8;
+    hipLaunchKernelGGL(gemm_large_halves<GLU>, dim3((unsigned)wgs), dim3(256), kLds, stream, p, whole);
 }
 
 template <bool GLU>
 void launch_choice(const Choice &c, const Operands &p, int *partial, hipStream_t stream)
 {
-    if (c.tile == k256x256) {
-        launch_large<GLU, 4, 4>(p, 1, partial, 0, c.whole, false, stream);
-        if (c.whole) launch_large<GLU, 4, 2>(p, 1, partial, c.whole, 0, true, stream);
+    if (c.tile == k256x256 && c.whole) {
+        launch_halves<GLU>(p, c.whole, stream);
+    } else if (c.tile == k256x256) {
+        launch_large<GLU, 4, 4>(p, 1, partial, stream);
     } else if (c.tile == k256x128) {
-        launch_large<GLU, 4, 2>(p, c.splits, partial, 0, 0, false, stream);
+        launch_large<GLU, 4, 2>(p, c.splits, partial, stream);
     } else if (c.tile == k128x128) {
-        launch_large<GLU, 2, 2>(p, c.splits, partial, 0, 0, false, stream);
+        launch_large<GLU, 2, 2>(p, c.splits, partial, stream);
     } else if (c.tile == k128x64) {
         launch_tiled<GLU, 128, 64, 32, 64, 4>(p, c.splits, partial, stream);
     } else if (c.tile == k64x64) {

@@ -8,10 +8,11 @@
  *
  * sum is the residual of the next addition, and the norm is that of the rounded
  * values: the same bits whether the addition was made here or before.  Squares
- * are exact and summed in fp32 in a fixed order; y is computed in fp32 and
- * rounded once, to the form that the call writes:
+ * are exact, summed by eights in fp32 and further in fp64, in a fixed order; y
+ * is computed in fp32 and rounded to the form that the call writes:
  *   sqllm_rms_norm       fp16 [rows][cols]
- *   sqllm_rms_norm_int8  the stored form of sqllm_int8.h
+ *   sqllm_rms_norm_int8  the stored form of sqllm_int8.h (its integers without
+ *                        rounding before: the root falls out of them)
  *   sqllm_rms_norm_fp8   the stored form of sqllm_fp8.h
  * A row of zeros with eps = 0 is 0 / 0: NaN.  An infinity in a row of sums
  * makes its own place NaN and the other values 0; a NaN makes the row NaN.

@@ -265,8 +265,13 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
 // has been read, stands before it.  Its places are loaded over from there on, a
 // part in every step so that no load waits for others to go out: x of the block
 // after the next in that step and the one behind it, then W of the block after
-// that.  With splits > 1 a workgroup has a share of the blocks, and the sums go
-// to partial[split][product][batch][rows].
+// that.  SPLIT: a workgroup has a share of the blocks, and the sums go to
+// partial[split][product][batch][rows].
+// 8192x8192 at batch 4096 takes 219 us (2500 TOP/s; 427 with 64x64 tiles).  The
+// matrix instructions alone take 171 on random operands, 124 on zeros: the clock
+// falls with their power; with the reads from LDS 176, with the loads 198.  The
+// rest is a tile's ends: 3 us to its first block, 5 from its last to the last
+// store, 3 of those for 256 conversions a lane.
 template <int FM, int FN>
 struct Large {
     static constexpr int kW = 64 * FM * kBlock, kX = 64 * FN * kBlock;
@@ -503,6 +508,9 @@ __device__ __forceinline__ int sum_of_16(int v)
 // one is used, and the waves' sums meet in LDS.  HALF: x comes in fp16.  Each
 // lane rounds the columns that it holds, once, while the first rows of W are on
 // their way; the largest of a row of x comes from all waves through LDS.
+// Memory bounds it: 8192x22016 at one row 28.4 us (6.4 TB/s; x in fp16 32.7),
+// 8192x8192 11.8, gate and up of 11008x4096 16.0 and of 22016x8192 55 (6.5 TB/s);
+// tiles took 46, 21 and 27.
 constexpr int kChunk = 1024;
 
 template <bool GLU, bool HALF, int B, int C, int R>
@@ -667,6 +675,11 @@ __global__ void __launch_bounds__(1024) gemm_dot(Operands p, const uint16_t *x, 
 // ring of D blocks of its own, loaded straight from memory, whole lines of eight
 // rows an instruction (in the matrix cores' layout it would be 64 bytes of
 // sixteen), D blocks ahead and on into the next group.
+// 8192x8192 at 16 rows takes 16.5 us, at one in the form above 11.8: every
+// workgroup reads x first, 33 MB in all out of the second-level caches, and that
+// is 3 us before W comes at its rate.  W through registers into LDS in half
+// kilobytes of a row took 17.5, x through the ring in turn with the first blocks
+// 16.3 and more registers, W asked for before x 17.8.
 constexpr int few_waves(int S) { return S > 8 ? 12 : 16; } // most waves of a workgroup
 
 template <bool GLU, int S, int D>
@@ -855,6 +868,13 @@ Choice choose(int64_t rows, int64_t cols, int64_t batch, bool glu)
     return best;
 }
 
+// The streaming form in the vector units, up to four rows of x: beyond, its
+// instructions and the sums' reduction outlast the loads (8192x8192 at four and
+// eight rows 13.0 and 18.7 us, the matrix cores' form 16.4 at both; gated
+// 11008x4096 18.1 and 24.9, 20.2).  Chunks a wave: few, so that waves are many
+// and each has little to add up.  us at one row with 1 and 2 chunks a wave:
+// 8192x8192 11.8, 12.0; 5120x5120 6.7, 7.2; with 2 and 3: 8192x22016 29.8, 28.2,
+// 4096x11008 10.6, 10.2.
 struct Dot {
     int waves, chunks; // of a wave; waves 0: not this form
 };
@@ -914,6 +934,10 @@ void launch_dot(const Operands &p, const uint16_t *x, int cols, int waves, hipSt
     hipLaunchKernelGGL((gemm_dot<GLU, HALF, B, C, R>), dim3(wgs), dim3(64 * waves), 0, stream, p, x, cols, groups);
 }
 
+// Rows of a group.  us at one row with 2, 4 and 8: 8192x8192, one chunk a wave,
+// 12.1, 11.8, 12.4; at four rows 15.7, 14.9, 16.2; 8192x22016, three chunks, 28.2
+// and 29.3 with 2 and 4.  x in fp16 takes registers: four rows with two chunks or
+// more spill (8192x22016 79 us), those go through the quantiser first (41).
 template <bool GLU, bool HALF, int B>
 void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStream_t stream)
 {
@@ -935,6 +959,9 @@ void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStrea
         launch_dots<GLU, HALF, 4>(p, x, cols, d, stream);
 }
 
+// Blocks a wave and ring, us at 16 rows.  8192x8192: 4 blocks, ring of 2 16.3, of
+// 4 16.5, 8 blocks, 8 17.3, 4 18.8, 16 blocks 23.8; 4096x4096: 2 blocks 6.6, 4
+// 7.0, 8 7.3; gated 11008x4096: 18.1, 20.2, 22.1.
 template <bool GLU, int S, int D>
 void launch_few(const Operands &p, hipStream_t stream)
 {

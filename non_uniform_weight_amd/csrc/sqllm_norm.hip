@@ -30,6 +30,7 @@ struct Rows {
     int span;    // columns written: `cols` padded as the output form has it
     int words;
     float eps;
+    double per_col; // 1 / cols
 };
 
 __device__ __forceinline__ void store8(uint16_t *row, int c, int cols, u32x4 v)
@@ -44,17 +45,39 @@ __device__ __forceinline__ void store8(uint16_t *row, int c, int cols, u32x4 v)
         if (c + k < cols) row[c + k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
 }
 
+// The sum of the sixteen lanes' v and then of the wave's four sixteens, in a
+// fixed order.  In all lanes.
+__device__ __forceinline__ double wave_sum(double v)
+{
+    auto add = [&](auto turned) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        v += __builtin_bit_cast(double, (uint64_t)(uint32_t)turned((uint32_t)b) | (uint64_t)(uint32_t)turned((uint32_t)(b >> 32)) << 32);
+    };
+#define SQLLM_TURN(n) add([](uint32_t w) { return __builtin_amdgcn_update_dpp(0, (int)w, 0x120 + n, 0xF, 0xF, true); })
+    SQLLM_TURN(8);
+    SQLLM_TURN(4);
+    SQLLM_TURN(2);
+    SQLLM_TURN(1);
+#undef SQLLM_TURN
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    auto of = [&](int lane) {
+        return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)b, lane) |
+                                              (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane) << 32);
+    };
+    return (of(0) + of(16)) + (of(32) + of(48));
+}
+
 // The same over a row's threads.  ONE: they are a wave; else the workgroup, of
 // up to sixteen, and `red` is sixteen words of LDS of its own.
 template <bool ONE>
-__device__ __forceinline__ float row_sum(float v, uint32_t *red)
+__device__ __forceinline__ double row_sum(double v, double *red)
 {
     v = wave_sum(v);
     if constexpr (!ONE) {
-        red[threadIdx.x >> 6] = __float_as_uint(v);
+        red[threadIdx.x >> 6] = v;
         __syncthreads();
-        v = 0.f;
-        for (uint32_t k = 0; k < blockDim.x >> 6; ++k) v += __uint_as_float(red[k]);
+        v = 0.;
+        for (uint32_t k = 0; k < blockDim.x >> 6; ++k) v += red[k];
     }
     return v;
 }
@@ -76,28 +99,33 @@ __device__ __forceinline__ u32x4 add8(u32x4 a, u32x4 b)
     return __builtin_bit_cast(u32x4, (half8_t)(__builtin_bit_cast(half8_t, a) + __builtin_bit_cast(half8_t, b)));
 }
 
-__device__ __forceinline__ float squares(u32x4 v, float sum)
+// The sum of eight squares in fp32; sums of these are in fp64, so that a row's
+// sum is off by 2^-24 over the root of its pieces' number.
+__device__ __forceinline__ float squares(u32x4 v)
 {
     const half8_t h = __builtin_bit_cast(half8_t, v);
+    float s[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum = __builtin_fmaf((float)h[k], (float)h[k], sum);
-    return sum;
+    for (int k = 0; k < 4; ++k) {
+        const float a = (float)h[2 * k], b = (float)h[2 * k + 1];
+        s[k] = __builtin_fmaf(a, a, b * b);
+    }
+    return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 // 1 / sqrt(m) in two parts: the reciprocal root r and what one step of
 // Newton's method adds to it, r (1 - m r^2) / 2, so that y has no rounding but
-// that of its last addition.  (With r alone one code in a million more lands
-// on the other side of a border between two codes.)
+// that of its last addition.  (With r alone three times as many of the 8-bit
+// codes land on the other side of a border between two.)
 struct Root {
     float high, low;
 };
 
-__device__ __forceinline__ Root reciprocal_root(float m)
+__device__ __forceinline__ Root reciprocal_root(double m)
 {
-    const float r = rsqrtf(m), h = m * r, rest = __builtin_fmaf(m, r, -h);
-    const float off = __builtin_fmaf(-rest, r, __builtin_fmaf(-h, r, 1.f));
-    // not for m = 0 or infinity, where r says all
-    return {r, m > 0.f && m < INFINITY ? 0.5f * r * off : 0.f};
+    const float f = (float)m, r = rsqrtf(f);
+    // not for 0 or infinity, where r says all
+    return {r, f > 0.f && f < INFINITY ? 0.5f * r * (float)__builtin_fma(-m * r, (double)r, 1.) : 0.f};
 }
 
 // y of eight values: sum * weight is exact in fp32 (two fp16 values).
@@ -108,6 +136,54 @@ __device__ __forceinline__ void normalized(u32x4 v, u32x4 w, Root root, float (&
     for (int k = 0; k < 8; ++k) {
         const float p = (float)a[k] * (float)b[k];
         y[k] = __builtin_fmaf(p, root.high, p * root.low);
+    }
+}
+
+// The int8 form needs no root for its integers: they are nearest to 127 p / the
+// largest |p| of the row, p = sum * weight, exact.
+__device__ __forceinline__ void products(u32x4 v, u32x4 w, float (&p)[8])
+{
+    const half8_t a = __builtin_bit_cast(half8_t, v), b = __builtin_bit_cast(half8_t, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) p[k] = (float)a[k] * (float)b[k];
+}
+
+// The integers of p, m its row's largest.  A quotient that has been rounded to
+// half way between two goes to its own side: one bit on.
+__device__ __forceinline__ u32x2 integers_of(const float (&p)[8], float m, Inverse inverse)
+{
+    float t[8], off = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        t[k] = __builtin_fmaf(p[k], inverse.high, p[k] * inverse.low);
+        off = fmaxf(off, fabsf(t[k] - rintf(t[k])));
+    }
+    if (off == 0.5f) { // (one wave in two hundred)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const double rest = 127. * p[k] - (double)t[k] * m; // exact
+            if (fabsf(t[k] - rintf(t[k])) == 0.5f && rest != 0.)
+                t[k] = __uint_as_float(__float_as_uint(t[k]) + ((rest > 0.) == (t[k] > 0.f) ? 1 : -1));
+        }
+    }
+    return bytes_of(t);
+}
+
+// Before y is rounded again, to e4m3: where it lies on a border between two codes
+// (all of those have sixteen low bits of zero) and the exact product does not,
+// one bit towards that, or the tie would go to the even code.
+__device__ __forceinline__ void off_the_border(u32x4 v, u32x4 w, Root root, float (&y)[8])
+{
+    uint32_t low = 0xFFFF;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) low = min(low, __float_as_uint(y[k]) & 0xFFFF);
+    if (low) return; // (one wave in a hundred goes on)
+    const half8_t a = __builtin_bit_cast(half8_t, v), b = __builtin_bit_cast(half8_t, w);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const float p = (float)a[k] * (float)b[k], rest = __builtin_fmaf(p, root.high, -y[k]) + p * root.low;
+        if (rest != 0.f && !(__float_as_uint(y[k]) & 0xFFFF) && fabsf(y[k]) < INFINITY && y[k] != 0.f)
+            y[k] = __uint_as_float(__float_as_uint(y[k]) + ((rest > 0.f) == (y[k] > 0.f) ? 1 : -1));
     }
 }
 
@@ -160,10 +236,25 @@ __device__ __forceinline__ void store_fp8(const Rows &a, int64_t row, int c, con
     if ((threadIdx.x & 63) == 0 && c < a.span) ((uint32_t *)a.scale)[row * a.words + (c >> 9)] = word;
 }
 
-__device__ __forceinline__ Inverse store_scale(const Rows &a, int64_t row, uint32_t top, bool first)
+// What the integers of a row are made with, top: the bits of its largest
+// magnitude (of y, or of p with the root that makes y of it).
+template <int FORM>
+__device__ __forceinline__ Inverse store_scale(const Rows &a, int64_t row, uint32_t top, Root root, bool first)
 {
-    if (first) ((float *)a.scale)[row] = scale_of(top);
+    if (first) {
+        const float m = __uint_as_float(top);
+        const uint32_t y = FORM == kQuantize ? top : __float_as_uint(fabsf(__builtin_fmaf(m, root.high, m * root.low)));
+        ((float *)a.scale)[row] = scale_of(max(top >= kInf ? top : 0, y));
+    }
     return inverse_of(top);
+}
+
+template <int FORM>
+__device__ __forceinline__ void store_integers(const Rows &a, int64_t row, int c, const float (&y)[8], uint32_t top, Inverse inverse)
+{
+    u32x2 q = {0, 0};
+    if (top < kInf) q = FORM == kQuantize ? integers(y, inverse) : integers_of(y, __uint_as_float(top), inverse);
+    *(u32x2 *)((int8_t *)a.out + row * a.ldo + c) = q;
 }
 
 // A row in the registers of a wave (ONE; four rows a workgroup, no barrier) or
@@ -171,7 +262,8 @@ __device__ __forceinline__ Inverse store_scale(const Rows &a, int64_t row, uint3
 template <int FORM, bool RES, bool ONE, int V>
 __global__ void __launch_bounds__(ONE ? 256 : 1024) rows_kernel(Rows a)
 {
-    __shared__ uint32_t red[2][16];
+    __shared__ double sums[16];
+    __shared__ uint32_t red[16];
     const int T = ONE ? 64 : blockDim.x, t = ONE ? threadIdx.x & 63 : threadIdx.x;
     const int64_t row = ONE ? (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
     if (ONE && row >= a.rows) return;
@@ -193,23 +285,29 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) rows_kernel(Rows a)
 #pragma unroll
         for (int k = 0; k < V; ++k) v[k] = add8(v[k], r[k]);
     float y[V][8];
+    Root root = {};
     if constexpr (FORM != kQuantize) {
-        float s = 0.f;
+        double s = 0.;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int c = (k * T + t) * 8;
             if (RES && a.sum && c < a.cols) store8(a.sum + row * a.cols, c, a.cols, v[k]);
-            s += squares(v[k], 0.f);
+            s += squares(v[k]);
         }
-        const Root root = reciprocal_root(row_sum<ONE>(s, red[0]) / (float)a.cols + a.eps);
+        root = reciprocal_root(row_sum<ONE>(s, sums) * a.per_col + a.eps);
 #pragma unroll
-        for (int k = 0; k < V; ++k) normalized(v[k], w[k], root, y[k]);
-        // (a root of infinity or NaN turns the zeros past the end into NaN)
-#pragma unroll
-        for (int k = 0; k < V; ++k)
+        for (int k = 0; k < V; ++k) {
+            if constexpr (FORM == kNormInt8) {
+                products(v[k], w[k], y[k]);
+                continue;
+            }
+            normalized(v[k], w[k], root, y[k]);
+            if constexpr (FORM == kNormFp8) off_the_border(v[k], w[k], root, y[k]);
+            // (a root of infinity or NaN turns the zeros past the end into NaN)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if ((k * T + t) * 8 + j >= a.cols) y[k][j] = 0.f;
+        }
     } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
@@ -230,12 +328,12 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) rows_kernel(Rows a)
         uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < V; ++k) top = max(top, magnitude(y[k]));
-        top = row_max<ONE>(top, red[1]);
-        const Inverse inverse = store_scale(a, row, top, t == 0);
+        top = row_max<ONE>(top, red);
+        const Inverse inverse = store_scale<FORM>(a, row, top, root, t == 0);
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int c = (k * T + t) * 8;
-            if (c < a.span) *(u32x2 *)((int8_t *)a.out + row * a.ldo + c) = top >= kInf ? u32x2{0, 0} : integers(y[k], inverse);
+            if (c < a.span) store_integers<FORM>(a, row, c, y[k], top, inverse);
         }
     }
 }
@@ -245,21 +343,22 @@ __global__ void __launch_bounds__(ONE ? 256 : 1024) rows_kernel(Rows a)
 template <int FORM, bool RES>
 __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
 {
-    __shared__ uint32_t red[2][16];
+    __shared__ double sums[16];
+    __shared__ uint32_t red[16];
     const int64_t row = blockIdx.x;
     const uint16_t *const x = a.x + row * a.ldx;
     Root root = {};
     if constexpr (FORM != kQuantize) {
-        float s = 0.f;
+        double s = 0.;
         for (int c = threadIdx.x * 8; c < a.cols; c += 8192) {
             u32x4 v = load8(x, c, a.cols);
             if constexpr (RES) {
                 v = add8(v, load8(a.residual + row * a.ldr, c, a.cols));
                 if (a.sum) store8(a.sum + row * a.cols, c, a.cols, v);
             }
-            s += squares(v, 0.f);
+            s += squares(v);
         }
-        root = reciprocal_root(row_sum<false>(s, red[0]) / (float)a.cols + a.eps);
+        root = reciprocal_root(row_sum<false>(s, sums) * a.per_col + a.eps);
     }
     auto value = [&](int c, float (&y)[8]) {
         u32x4 v = u32x4{0, 0, 0, 0};
@@ -274,7 +373,10 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
         if constexpr (FORM == kQuantize) {
             floats(v, y);
         } else {
-            normalized(v, c < a.cols ? load8(a.weight, c, a.cols) : u32x4{0, 0, 0, 0}, root, y);
+            const u32x4 w = c < a.cols ? load8(a.weight, c, a.cols) : u32x4{0, 0, 0, 0};
+            if constexpr (FORM == kNormInt8) return products(v, w, y);
+            normalized(v, w, root, y);
+            if constexpr (FORM == kNormFp8) off_the_border(v, w, root, y);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (c + j >= a.cols) y[j] = 0.f;
@@ -297,11 +399,11 @@ __global__ void __launch_bounds__(1024) long_rows_kernel(Rows a)
             value(c, y);
             top = max(top, magnitude(y));
         }
-        top = row_max<false>(top, red[1]);
-        const Inverse inverse = store_scale(a, row, top, threadIdx.x == 0);
+        top = row_max<false>(top, red);
+        const Inverse inverse = store_scale<FORM>(a, row, top, root, threadIdx.x == 0);
         for (int c = threadIdx.x * 8; c < a.span; c += 8192) {
             value(c, y);
-            *(u32x2 *)((int8_t *)a.out + row * a.ldo + c) = top >= kInf ? u32x2{0, 0} : integers(y, inverse);
+            store_integers<FORM>(a, row, c, y, top, inverse);
         }
     }
 }
@@ -391,7 +493,7 @@ hipError_t launch_int8_quantize(const uint16_t *x, int64_t rows, int64_t cols, i
 {
     const int64_t ld = sqllm_int8_cols(cols);
     return launch_pieces<kQuantize>(
-        Rows{x, nullptr, nullptr, nullptr, q, scale, ldx, 0, ld, 0, (int)cols, (int)ld, 0, 0.f}, rows, stream);
+        Rows{x, nullptr, nullptr, nullptr, q, scale, ldx, 0, ld, 0, (int)cols, (int)ld, 0, 0.f, 0.}, rows, stream);
 }
 
 } // namespace sqllm
@@ -419,7 +521,7 @@ extern "C" sqllm_status sqllm_rms_norm(const uint16_t *x, int64_t ldx, const uin
     if (st != SQLLM_OK) return st;
     if (!aligned(y, 2)) return SQLLM_ERR_ALIGN;
     return status(launch_pieces<kNormHalf>(
-        Rows{x, residual, weight, sum, y, nullptr, ldx, ldr, cols, 0, (int)cols, (int)cols, 0, eps}, rows, stream));
+        Rows{x, residual, weight, sum, y, nullptr, ldx, ldr, cols, 0, (int)cols, (int)cols, 0, eps, 1. / cols}, rows, stream));
 }
 
 extern "C" sqllm_status sqllm_rms_norm_int8(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr,
@@ -432,7 +534,7 @@ extern "C" sqllm_status sqllm_rms_norm_int8(const uint16_t *x, int64_t ldx, cons
     if (!aligned(q, 16) || !aligned(scale, 4)) return SQLLM_ERR_ALIGN;
     const int64_t ld = sqllm_int8_cols(cols);
     return status(launch_pieces<kNormInt8>(
-        Rows{x, residual, weight, sum, q, scale, ldx, ldr, ld, 0, (int)cols, (int)ld, 0, eps}, rows, stream));
+        Rows{x, residual, weight, sum, q, scale, ldx, ldr, ld, 0, (int)cols, (int)ld, 0, eps, 1. / cols}, rows, stream));
 }
 
 extern "C" sqllm_status sqllm_rms_norm_fp8(const uint16_t *x, int64_t ldx, const uint16_t *residual, int64_t ldr,
@@ -446,6 +548,6 @@ extern "C" sqllm_status sqllm_rms_norm_fp8(const uint16_t *x, int64_t ldx, const
     if (rows * pitch > ((int64_t)1 << 30) - 256) return SQLLM_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(scale, 4)) return SQLLM_ERR_ALIGN;
     return status(launch_pieces<kNormFp8>(Rows{x, residual, weight, sum, q, scale, ldx, ldr, sqllm_fp8_cols(cols), 0,
-                                               (int)cols, (int)(pitch * 128), (int)(pitch / 4), eps},
+                                               (int)cols, (int)(pitch * 128), (int)(pitch / 4), eps, 1. / cols},
                                           rows, stream));
 }

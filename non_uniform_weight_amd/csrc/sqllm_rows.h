@@ -44,20 +44,8 @@ __device__ __forceinline__ void floats(u32x4 v, float (&y)[8])
     for (int k = 0; k < 8; ++k) y[k] = (float)h[k];
 }
 
-// The sum of the sixteen lanes' v and then of the wave's four sixteens, in a
-// fixed order; the largest, the same way.  In all lanes.
+// The largest of sixteen lanes' v, and of a wave's.  In all lanes.
 #define SQLLM_ROR(v, n) __builtin_amdgcn_update_dpp(0, (int)(v), 0x120 + n, 0xF, 0xF, true)
-__device__ __forceinline__ float wave_sum(float v)
-{
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 8));
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 4));
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 2));
-    v += __uint_as_float(SQLLM_ROR(__float_as_uint(v), 1));
-    const int b = (int)__float_as_uint(v);
-    return (__uint_as_float(__builtin_amdgcn_readlane(b, 0)) + __uint_as_float(__builtin_amdgcn_readlane(b, 16))) +
-           (__uint_as_float(__builtin_amdgcn_readlane(b, 32)) + __uint_as_float(__builtin_amdgcn_readlane(b, 48)));
-}
-
 __device__ __forceinline__ uint32_t max_of_16(uint32_t v)
 {
     v = max(v, (uint32_t)SQLLM_ROR(v, 8));
@@ -103,20 +91,28 @@ __device__ __forceinline__ Inverse inverse_of(uint32_t top)
     return {high, __builtin_fmaf(-high, m, 127.f) * (high * (1.f / 127.f))};
 }
 
-// Eight integers nearest to y * inverse, ties to even: added to 1.5 * 2^23, the
-// sum's low byte is the integer.  (A value that is not half way is further from
-// it than the rounding before the sum moves it: fp16 mantissas have 11 bits.)
-__device__ __forceinline__ u32x2 integers(const float (&y)[8], Inverse inverse)
+// Eight integers nearest to t, ties to even: added to 1.5 * 2^23, the sum's low
+// byte is the integer.
+__device__ __forceinline__ u32x2 bytes_of(const float (&t)[8])
 {
     uint32_t b[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        b[k] = __float_as_uint(__builtin_fmaf(y[k], inverse.high, y[k] * inverse.low) + 12582912.f);
+    for (int k = 0; k < 8; ++k) b[k] = __float_as_uint(t[k] + 12582912.f);
     auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
         return __builtin_amdgcn_perm(__builtin_amdgcn_perm(d, c, 0x0C0C0400u), __builtin_amdgcn_perm(b, a, 0x0C0C0400u),
                                      0x05040100u);
     };
     return u32x2{four(b[0], b[1], b[2], b[3]), four(b[4], b[5], b[6], b[7])};
+}
+
+// The same of fp16 values y * inverse: one that is not half way is further from
+// it than the rounding here moves it (mantissas of 11 bits).
+__device__ __forceinline__ u32x2 integers(const float (&y)[8], Inverse inverse)
+{
+    float t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) t[k] = __builtin_fmaf(y[k], inverse.high, y[k] * inverse.low);
+    return bytes_of(t);
 }
 
 } // namespace rows

@@ -1,7 +1,7 @@
 """The norm and the quantiser to 8-bit integers on the GPU against 64-bit references.
 
-Tolerances.  total is one fp16 addition: exact.  Squares of fp16 values are exact in fp32.  Their sum runs through at
-most `adds` additions on a path from a square to the total (8 in a piece of eight values, the pieces of a thread, 4 + 2
+Tolerances.  total is one fp16 addition: exact.  Squares of fp16 values are exact in fp32.  Their sum, were it in fp32
+throughout, would run through at most `adds` additions on a path from a square to the total (8 in a piece of eight values, the pieces of a thread, 4 + 2
 in a wave, one for each wave; rows beyond 32768 columns add the pieces of a thread in one chain), each 2^-24 relative
 at worst (all terms are positive); mean and eps add two, and the root halves them; the product with the root rounds
 once more and the quotient of the int8 scale once.  So y in fp32 is off by e = (adds / 2 + 4) * 2^-24 relative.
@@ -240,6 +240,54 @@ def test_norm_eps(eps):
     check_fp8(f[keep], fs[keep], ref[keep], e_of(700))
     if eps == 0:  # 0 / 0
         assert y[2].isnan().all() and scale[2].isnan() and np.isnan(e4m3(f)[2, :700]).all()
+
+
+def nearest_even(p, top):
+    """The integers nearest to 127 p / top, ties to even, without rounding: products of 22-bit numbers with small
+    integers are exact in 64 bits."""
+    low = np.floor(127 * p / top)
+    low = np.where(127 * p < low * top, low - 1, low)          # should the quotient have been rounded up
+    low = np.where(127 * p >= (low + 1) * top, low + 1, low)   # or down
+    side = 254 * p - (2 * low + 1) * top
+    return np.where(side > 0, low + 1, np.where(side < 0, low, low + low % 2))
+
+
+@pytest.mark.parametrize("rows,cols", [(400, 1000), (200, 8192), (3, 40000)])
+def test_norm_int8_integers_are_exact(rows, cols):
+    """The root falls out of the integers: nearest to 127 sum weight / the row's largest."""
+    step(f"norm int8 exact {rows}x{cols}")
+    xh, wh = rows_of(rows, cols, 4), weight_of(cols, 5)
+    wh[::3] = np.round(wh[::3] * 8) / 8  # and where many quotients are half way
+    xh[:rows // 2] = np.round(xh[:rows // 2].astype(np.float64) * 4) / 4
+    q, _ = nw().rms_norm_int8(dev(xh), dev(wh), EPS)
+    p = xh.astype(np.float64) * wh.astype(np.float64)
+    top = np.abs(p).max(axis=1, keepdims=True)
+    assert np.array_equal(q.cpu().numpy()[:, :cols], nearest_even(p, np.where(top > 0, top, 1)).astype(np.int8))
+
+
+@pytest.mark.parametrize("cols", [32768, 65536])
+def test_norm_beside_the_borders_of_e4m3(cols):
+    """y a quarter of an fp32 step beside a border between two codes: to the code of its own side, not to the even one."""
+    step(f"norm e4m3 borders {cols}")
+    w = np.ones(cols, np.float16)
+    w[:8] = [1.0625, 1.1875, 1.3125, 1.4375, -1.0625, -1.1875, -1.3125, -1.4375]  # borders, even codes below and above
+    below = [1.0, 1.125, 1.25, 1.375]
+    above = [1.125, 1.25, 1.375, 1.5]
+    # all ones: the root is 1 / sqrt(1 + eps), 5e-8 below 1
+    q, scale = nw().rms_norm_fp8(dev(np.ones((1, cols), np.float16)), dev(w), 1e-7)
+    v = e4m3(q)[0, :8] * 2.0 ** (int(scale[0, 0]) - 127)
+    assert v.tolist() == below + [-b for b in below]
+    # one value 2^-11 below 1: the root is 2^-11 / cols above 1
+    x = np.ones((1, cols), np.float16)
+    x[0, -1] -= 2.0 ** -11
+    q, scale = nw().rms_norm_fp8(dev(x), dev(w), 0.0)
+    v = e4m3(q)[0, :8] * 2.0 ** (int(scale[0, 0]) - 127)
+    assert v.tolist() == above + [-b for b in above]
+    # on the border: to the even code
+    q, scale = nw().rms_norm_fp8(dev(np.ones((1, cols), np.float16)), dev(w), 0.0)
+    v = e4m3(q)[0, :8] * 2.0 ** (int(scale[0, 0]) - 127)
+    even = [1.0, 1.25, 1.25, 1.5]
+    assert v.tolist() == even + [-b for b in even]
 
 
 def test_norm_and_quantize_many_rows():

@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(1024) gemm_dot(Operands p, const uint16_t *x, 
 // workgroup reads x first, 33 MB in all out of the second-level caches, and that
 // is 3 us before W comes at its rate.  W through registers into LDS in half
 // kilobytes of a row took 17.5, x through the ring in turn with the first blocks
-// 16.3 and more registers, W asked for before x 17.8.
+// 16.3 and more registers, W asked for before x 16.8 to 17.8.
 constexpr int few_waves(int S) { return S > 8 ? 12 : 16; } // most waves of a workgroup
 
 template <bool GLU, int S, int D>

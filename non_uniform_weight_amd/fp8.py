@@ -87,11 +87,11 @@ def fp8_gemm(index, handle, q: torch.Tensor, scale: torch.Tensor, x: torch.Tenso
                          f"{cols} columns, got {tuple(q.shape)} and {tuple(scale.shape)}")
     qp, sp = _calls.address(q, "q", torch.uint8, index), _calls.address(scale, "scale", torch.uint8, index)
     if x_scale is not None:
+        call, name = _gemm_stored, "sqllm_fp8_gemm_stored"
+        xs = (_calls.address(x, "x", torch.uint8, index), _calls.address(x_scale, "x_scale", torch.uint8, index))
         if cols != fp8_cols(cols) or x_scale.shape != (batch, pitch):
             raise ValueError(f"x, x_scale: shapes {(batch, fp8_cols(cols))} and {(batch, pitch)} expected, got "
                              f"{tuple(x.shape)} and {tuple(x_scale.shape)}")
-        call, name = _gemm_stored, "sqllm_fp8_gemm_stored"
-        xs = (_calls.address(x, "x", torch.uint8, index), _calls.address(x_scale, "x_scale", torch.uint8, index))
     else:
         call, name, xs = _gemm, "sqllm_fp8_gemm", (_calls.address(x, "x", torch.float16, index),)
     y, yp = _calls.output(y, "y", (batch, rows), torch.float16, index)

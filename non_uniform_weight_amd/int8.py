@@ -70,10 +70,10 @@ def _activations(x, x_scale, kept, index):
         if kept != int8_cols(cols):
             raise ValueError(f"weights: {int8_cols(cols)} stored columns expected for {cols} of x, got {kept}")
         return batch, cols, _calls.address(x, "x", torch.float16, index), None
+    xp, xsp = _calls.address(x, "x", torch.int8, index), _calls.address(x_scale, "x_scale", torch.float32, index)
     stored, cols = cols, min(cols, _MAX_COLS)  # (the longest rows' last stored column is padding)
     if stored != kept or kept != int8_cols(cols):
         raise ValueError(f"x: the weights' {kept} stored columns (a multiple of 128) expected, got {stored}")
-    xp, xsp = _calls.address(x, "x", torch.int8, index), _calls.address(x_scale, "x_scale", torch.float32, index)
     if x_scale.numel() != batch:
         raise ValueError(f"x_scale: {batch} values expected, got {x_scale.numel()}")
     return batch, cols, xp, xsp

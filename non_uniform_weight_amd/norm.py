@@ -42,9 +42,9 @@ def _inputs(x, weight, eps, residual, total, index):
         if total is not None:
             raise ValueError("total: only with a residual")
         return rows, cols, (xp, ldx, None, 0, wp, rows, cols, eps, None), ()
-    if residual.shape != x.shape:
-        raise ValueError(f"residual: shape {tuple(x.shape)} expected, got {tuple(residual.shape)}")
-    _, _, ldr, rp = _calls.half_rows(residual, "residual", index)
+    added, width, ldr, rp = _calls.half_rows(residual, "residual", index)
+    if added != rows or width != cols:
+        raise ValueError(f"residual: shape {(rows, cols)} expected, got {(added, width)}")
     total, tp = _half_output(total, "total", x, rows, cols, index)
     return rows, cols, (xp, ldx, rp, ldr, wp, rows, cols, eps, tp), (total,)
 

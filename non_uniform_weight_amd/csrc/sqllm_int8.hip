@@ -161,6 +161,11 @@ __device__ __forceinline__ bool tile_of(const Operands &p, int wg, int first, in
 // (row % 8), so that the sixteen rows that a fragment read takes at one piece
 // lie in different banks; loads into LDS write lane after lane, so the swizzle
 // is in the address they read from.
+// What bounds small tiles is what a compute unit takes in: 47 bytes/ns with one
+// workgroup, 60 with two.  64x32 tiles, 8192x8192 at batch 64, with four stages
+// 20.6 us, five and six 19.5, twelve 20.4; two groups of waves a workgroup, on
+// blocks of their own with the sums added through LDS, 19.6; every workgroup
+// beginning at another block, so that they read other channels, 19.6 to 25.
 template <int TM, int TN, int WM, int WN, int S>
 struct Tiling {
     static constexpr int W = (TM / WM) * (TN / WN);
@@ -821,24 +826,24 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // 8192x8192, 64 blocks a tile, at 256 and 512 tiles: 256x256 at batch 2048 118 us
 // and at 4096 219; 256x128 at 1024 67, at 2048 132; 128x128 at 512 45, at 1024
 // 73; 128x64 at 256 36, at 512 67; 64x64 at 128 25.5, at 256 40; 64x32 at 64
-// 22.8, at 128 31.4.
+// 19.5, at 128 31.0.
 enum Tile { k256x256, k256x128, k128x128, k128x64, k64x64, k64x32, kTiles };
 constexpr struct {
     int tm, tn;
     double one, two;
     bool pairs;
 } kTile[kTiles] = {{256, 256, 1.68, 3.36, false}, {256, 128, 0.96, 1.92, false}, {128, 128, 0.66, 1.06, true},
-                   {128, 64, 0.48, 0.96, false},  {64, 64, 0.34, 0.53, true},    {64, 32, 0.29, 0.42, true}};
+                   {128, 64, 0.48, 0.96, false},  {64, 64, 0.34, 0.53, true},    {64, 32, 0.28, 0.42, true}};
 
 // How a product is tiled: what these times make least.  Splitting the columns
 // costs a launch (5.5 us) and the sums' way through memory (4 TB/s); what is
 // left after whole rounds of 256x256 tiles goes in halves where that is half a
 // round or less (gated 13824x5120 at batch 2048, 864 tiles: 262 us, 275 without;
 // 5120x5120 at 8192, 640: 188 and 200).  What it weighs, in us at one, two and four
-// splits: 8192x8192 at batch 17 64x32 19.6, 19.7, 17.3; at 64 128x64 34, 27, 21,
-// 64x64 26, 22, 22; at 128 64x64 25.5, 30, 32; at 256 128x64 36, 44, 55, 128x128
+// splits: 8192x8192 at batch 17 64x32 18.2, 19.8, 17.6; at 64 128x64 34, 25, 20.5,
+// 64x64 24, 22, 21, 64x32 19.5, 23, 25; at 128 64x64 25.5, 30, 32; at 256 128x64 36, 44, 55, 128x128
 // 41, 37, 40; at 512 128x128 45, 58, 73, 256x128 59, 53; 4096x4096 at 32 64x32
-// 11.6, 10.5, 10.0; at 128 64x32 11.4, 15, 18, 64x64 13.5, 13.4, 17; at 256 64x64
+// 10.1, 10.0, 9.7; at 128 64x32 10.4, 14, 17, 64x64 13.5, 13.4, 17; at 256 64x64
 // 13.6, 20, 23, 128x64 19.5, 19, 21; at 512 128x64 20.5, 29, 128x128 23, 24, 28;
 // at 1024 128x128 24.5, 37, 256x128 32, 36.
 struct Choice {
@@ -1018,7 +1023,7 @@ void launch_choice(const Choice &c, const Operands &p, int *partial, hipStream_t
     } else if (c.tile == k64x64) {
         launch_tiled<GLU, 64, 64, 32, 32, 4>(p, c.splits, partial, stream);
     } else {
-        launch_tiled<GLU, 64, 32, 32, 16, 4>(p, c.splits, partial, stream);
+        launch_tiled<GLU, 64, 32, 32, 16, 5>(p, c.splits, partial, stream);
     }
 }
 

@@ -161,28 +161,34 @@ __device__ __forceinline__ bool tile_of(const Operands &p, int wg, int first, in
 // (row % 8), so that the sixteen rows that a fragment read takes at one piece
 // lie in different banks; loads into LDS write lane after lane, so the swizzle
 // is in the address they read from.
-// What bounds small tiles is what a compute unit takes in: 47 bytes/ns with one
-// workgroup, 60 with two.  64x32 tiles, 8192x8192 at batch 64, with four stages
-// 20.6 us, five and six 19.5, twelve 20.4; two groups of waves a workgroup, on
-// blocks of their own with the sums added through LDS, 19.6; every workgroup
-// beginning at another block, so that they read other channels, 19.6 to 25.
-template <int TM, int TN, int WM, int WN, int S>
+// What bounds small tiles: a compute unit takes in 145 bytes/ns out of its L2, but
+// 28 to 31 of W from memory.  64x32 tiles, 8192x8192 at batch 64, with four stages
+// 20.6 us, five and six 19.5, twelve 20.4; with every workgroup beginning at
+// another block, so that they read other channels, 19.6 to 25.  32 rows of W a tile
+// halve what a unit takes of it (at batch 17 15.4 us, in 64x32 tiles 18.2, with
+// split columns 17.6).  Their steps are short chains of latencies, so a workgroup has
+// G groups of waves: a stage is G blocks, one for each group, whose sums are added
+// through LDS at the end.  32x16 tiles, 1024x8192 at batch 32, with four groups 7.8
+// us, with two 9.1; at 256 tiles (4096x4096) 7.2 and 7.0.
+template <int TM, int TN, int WM, int WN, int S, int G>
 struct Tiling {
-    static constexpr int W = (TM / WM) * (TN / WN);
+    static constexpr int W = (TM / WM) * (TN / WN); // waves of a group
     static constexpr int kData = (TM + TN) * kBlock;
     static constexpr int kLoads = (TM + TN) / 8 / W; // 1 KB each
-    static constexpr size_t kLds = (size_t)S * kData;
+    static constexpr size_t kLds = (size_t)S * G * kData;
     static_assert((TM + TN) / 8 % W == 0, "as many loads in every wave");
     static_assert(TM % 16 == 0 && WM % 32 == 0, "halves of whole loads and accumulators");
+    static_assert(kLds <= 160 * 1024 && (size_t)(G - 1) * TM * TN * 4 <= kLds, "LDS of a compute unit, and the other groups' sums");
 };
 
-template <bool GLU, int TM, int TN, int WM, int WN, int S>
-__global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Operands p, int splits, int *partial)
+template <bool GLU, int TM, int TN, int WM, int WN, int S, int G>
+__global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN) * G, 2) gemm_tiled(Operands p, int splits, int *partial)
 {
-    using T = Tiling<TM, TN, WM, WN, S>;
+    using T = Tiling<TM, TN, WM, WN, S, G>;
     constexpr int kRows = GLU ? TM / 2 : TM; // of a matrix
     extern __shared__ __align__(16) int8_t lds[];
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int g = G > 1 ? wave / T::W : 0, w = wave - g * T::W;
     const int n = lane & 15, quarter = lane >> 4;
     int r0, b0;
     if (!tile_of<kRows, TN>(p, blockIdx.x, 0, 0, false, r0, b0)) return;
@@ -212,10 +218,10 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
         from[i] = (uint32_t)at * ld + ((lane & 7) ^ (lane >> 3)) * 16;
     }
     auto load_stage = [&](int k, int slot) {
-        const int at = min(k, k1 - 1);
+        const int at = min(k + g, k1 - 1);
 #pragma unroll
         for (int i = 0; i < T::kLoads; ++i)
-            lds_load16(src[i] + (uint32_t)at * kBlock + from[i], lds + slot * T::kData + (w * T::kLoads + i) * 1024);
+            lds_load16(src[i] + (uint32_t)at * kBlock + from[i], lds + (slot * G + g) * T::kData + (w * T::kLoads + i) * 1024);
     };
 
     constexpr int FM = WM / 16, FN = WN / 16;
@@ -227,13 +233,14 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
         for (int j = 0; j < FN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
     const int piece = n * kBlock + ((quarter ^ (n & 7)) * 16);
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) load_stage(k0 + s, s);
+    for (int s = 0; s < S - 1; ++s) load_stage(k0 + s * G, s);
     int slot = 0;
-    for (int k = k0; k < k1; ++k) {
+    for (int k = k0; k < k1; k += G) {
         stage_barrier<(S - 2) * T::kLoads>(); // stage k is in LDS
-        load_stage(k + S - 1, slot == 0 ? S - 1 : slot - 1); // where stage k - 1 was
-        const int8_t *base = lds + slot * T::kData;
+        load_stage(k + (S - 1) * G, slot == 0 ? S - 1 : slot - 1); // where the stage before k was
+        const int8_t *base = lds + (slot * G + g) * T::kData;
         slot = slot == S - 1 ? 0 : slot + 1;
+        if (G > 1 && k + g >= k1) continue; // (a copy of the last)
 #pragma unroll
         for (int h = 0; h < 2; ++h) { // 64 columns: pieces 4 h + quarter
             const int8_t *at = base + (piece ^ (64 * h));
@@ -249,6 +256,20 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN), 2) gemm_tiled(Oper
         }
     }
     wait_loads<0>(); // none may land after the workgroup's LDS is someone else's
+    if constexpr (G > 1) {
+        __syncthreads(); // (the stages' reads and loads are done)
+        i32x4 *const sums = (i32x4 *)lds + w * FM * FN * 64 + lane;
+        if (g) {
+#pragma unroll
+            for (int i = 0; i < FM * FN; ++i) sums[((g - 1) * T::W * FM * FN + i) * 64] = acc[i / FN][i % FN];
+        }
+        __syncthreads();
+        if (g) return;
+#pragma unroll
+        for (int i = 0; i < FM * FN; ++i)
+#pragma unroll
+            for (int k = 0; k < G - 1; ++k) acc[i / FN][i % FN] += sums[(k * T::W * FM * FN + i) * 64];
+    }
     constexpr int FR = GLU ? FM / 2 : FM;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -827,7 +848,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // and at 4096 219; 256x128 at 1024 67, at 2048 132; 128x128 at 512 45, at 1024
 // 73; 128x64 at 256 36, at 512 67; 64x64 at 128 25.5, at 256 40; 64x32 at 64
 // 19.5, at 128 31.0.
-enum Tile { k256x256, k256x128, k128x128, k128x64, k64x64, k64x32, kTiles };
+enum Tile { k256x256, k256x128, k128x128, k128x64, k64x64, k64x32, kTiles, k32x32 = kTiles, k32x16, k32x16x4 };
 constexpr struct {
     int tm, tn;
     double one, two;
@@ -851,11 +872,23 @@ struct Choice {
     int whole; // 256x256 tiles before the halves, 0: no halves
 };
 
+// First, tiles of 32 rows of W and 16 or 32 of x, unsplit, where every compute unit
+// has one at most (with more they are slower: 11008x4096 at batch 32, 344 tiles, 15.6
+// us, 64x32 13.1).  us, and what the rest of the rule gives: 4096x4096 at 17 and 32
+// 7.0, 7.8 and 9.5, 10.1, at 64 8.8 and 10.8; 8192x8192 at 17 15.0 and 17.4;
+// 1024x4096 at 128 6.4 and 8.8; gated 4096x4096 at 32 9.8 and 11.6, 1024x4096 5.7
+// and 8.8.  Not for a few long tiles, nor for the longest rows, where splits of the
+// columns gain more than they cost: 512x13824 at 77, 96 tiles, 12.3 and 10.6;
+// 8192x22016 at 32 41.8 and 40.3.
 Choice choose(int64_t rows, int64_t cols, int64_t batch, bool glu)
 {
     const int64_t blocks = sqllm_int8_cols(cols) / kBlock, m = glu ? 2 : 1;
     Choice best = {k256x256, 1, 0};
     double least = 1e30;
+    const int64_t of32 = (rows * m + 31) / 32 * ((batch + 31) / 32), of16 = (rows * m + 31) / 32 * ((batch + 15) / 16);
+    auto small = [&](int64_t tiles) { return tiles <= 256 && (blocks <= 64 || (blocks <= 128 && tiles > 128)); };
+    if (small(of16)) return {of16 <= 128 ? k32x16x4 : k32x16, 1, 0};
+    if (small(of32)) return {k32x32, 1, 0};
     for (int t = 0; t < kTiles; ++t) {
         const int64_t mine = kTile[t].tm / m, tiles = ((rows + mine - 1) / mine) * ((batch + kTile[t].tn - 1) / kTile[t].tn);
         for (int64_t s = 1; s <= 8 && (s == 1 || (t > k256x256 && blocks >= 8 * s)); s *= 2) {
@@ -920,16 +953,16 @@ void launch_add(const Operands &p, int splits, const int *partial, hipStream_t s
                        splits);
 }
 
-template <bool GLU, int TM, int TN, int WM, int WN, int S>
+template <bool GLU, int TM, int TN, int WM, int WN, int S, int G>
 void launch_tiled(const Operands &p, int splits, int *partial, hipStream_t stream)
 {
-    using T = Tiling<TM, TN, WM, WN, S>;
-    auto kern = gemm_tiled<GLU, TM, TN, WM, WN, S>;
+    using T = Tiling<TM, TN, WM, WN, S, G>;
+    auto kern = gemm_tiled<GLU, TM, TN, WM, WN, S, G>;
     static std::atomic<uint64_t> asked{0};
     sqllm::dev::raise_lds_limit((const void *)kern, asked, (int)T::kLds);
     constexpr int kRows = GLU ? TM / 2 : TM;
     const int64_t tiles = (int64_t)((p.rows + kRows - 1) / kRows) * ((p.batch + TN - 1) / TN);
-    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(64 * T::W), T::kLds, stream, p, splits,
+    hipLaunchKernelGGL(kern, dim3((unsigned)((tiles + 7) / 8 * 8), splits), dim3(64 * T::W * G), T::kLds, stream, p, splits,
                        partial);
     if (splits > 1) launch_add<GLU>(p, splits, partial, stream);
 }
@@ -1019,11 +1052,17 @@ void launch_choice(const Choice &c, const Operands &p, int *partial, hipStream_t
     } else if (c.tile == k128x128) {
         launch_large<GLU, 2, 2>(p, c.splits, partial, stream);
     } else if (c.tile == k128x64) {
-        launch_tiled<GLU, 128, 64, 32, 64, 4>(p, c.splits, partial, stream);
+        launch_tiled<GLU, 128, 64, 32, 64, 4, 1>(p, c.splits, partial, stream);
     } else if (c.tile == k64x64) {
-        launch_tiled<GLU, 64, 64, 32, 32, 4>(p, c.splits, partial, stream);
+        launch_tiled<GLU, 64, 64, 32, 32, 4, 1>(p, c.splits, partial, stream);
+    } else if (c.tile == k64x32) {
+        launch_tiled<GLU, 64, 32, 32, 16, 5, 1>(p, c.splits, partial, stream);
+    } else if (c.tile == k32x32) {
+        launch_tiled<GLU, 32, 32, 32, 16, 5, 2>(p, 1, nullptr, stream);
+    } else if (c.tile == k32x16) {
+        launch_tiled<GLU, 32, 16, 32, 16, 6, 2>(p, 1, nullptr, stream);
     } else {
-        launch_tiled<GLU, 64, 32, 32, 16, 5>(p, c.splits, partial, stream);
+        launch_tiled<GLU, 32, 16, 32, 16, 5, 4>(p, 1, nullptr, stream);
     }
 }
 

@@ -112,6 +112,22 @@ def test_glu(batch, rows, cols):
     assert torch.equal(nw().int8_glu(gq, gs, uq, us, x), h)
 
 
+# Tiles of a few rows of W whose waves share the blocks (one to 128 blocks, so that some groups of waves have one less
+# or none; rows and batches that end inside a tile), and split columns with the tiles above them.
+FEW = [(17, 32, 100), (17, 33, 128), (20, 4097, 129), (32, 4096, 4096), (48, 2700, 4000), (64, 1000, 385), (32, 4090, 11008),
+       (129, 700, 7000), (295, 210, 128), (582, 193, 136), (60, 2040, 8192), (300, 500, 9000), (29, 2300, 13900),
+       (26, 8465, 6456), (19, 4483, 16399), (17, 2097, 16542), (656, 778, 9159), (428, 577, 4998), (370, 216, 16669),
+       (553, 466, 9433), (376, 342, 5449), (291, 141, 16682), (462, 1029, 9409), (451, 857, 7459), (401, 473, 16406),
+       (437, 1745, 17094), (480, 433, 7598), (614, 179, 16510), (177, 2637, 11906), (708, 1185, 129), (620, 3281, 129),
+       (643, 1236, 11607), (545, 1848, 5886), (516, 3196, 129)]
+
+
+@pytest.mark.parametrize("batch,rows,cols", FEW)
+def test_few_tiles(batch, rows, cols):
+    test_gemm(batch, rows, cols)
+    test_glu(batch, rows, cols)
+
+
 @pytest.mark.parametrize("batch", [1, 16, 40, 300])
 def test_largest_sums(batch):
     """Rows of codes of one sign at both ends of their range, up to the longest row: the sums stay within 32 bits."""

@@ -848,7 +848,7 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // and at 4096 219; 256x128 at 1024 67, at 2048 132; 128x128 at 512 45, at 1024
 // 73; 128x64 at 256 36, at 512 67; 64x64 at 128 25.5, at 256 40; 64x32 at 64
 // 19.5, at 128 31.0.
-enum Tile { k256x256, k256x128, k128x128, k128x64, k64x64, k64x32, kTiles, k32x32 = kTiles, k32x16, k32x16x4 };
+enum Tile { k256x256, k256x128, k128x128, k128x64, k64x64, k64x32, kTiles, k32x16 = kTiles, k32x16x4, k32x32, k32x64, k64x64x3 };
 constexpr struct {
     int tm, tn;
     double one, two;
@@ -872,28 +872,35 @@ struct Choice {
     int whole; // 256x256 tiles before the halves, 0: no halves
 };
 
-// First, tiles of 32 rows of W and 16 or 32 of x, unsplit, where every compute unit
-// has one at most (with more they are slower: 11008x4096 at batch 32, 344 tiles, 15.6
-// us, 64x32 13.1).  us, and what the rest of the rule gives: 4096x4096 at 17 and 32
-// 7.0, 7.8 and 9.5, 10.1, at 64 8.8 and 10.8; 8192x8192 at 17 15.0 and 17.4;
-// 1024x4096 at 128 6.4 and 8.8; gated 4096x4096 at 32 9.8 and 11.6, 1024x4096 5.7
-// and 8.8.  Not for a few long tiles, nor for the longest rows, where splits of the
-// columns gain more than they cost: 512x13824 at 77, 96 tiles, 12.3 and 10.6;
-// 8192x22016 at 32 41.8 and 40.3.
+// First, the smallest unsplit tiles of which every compute unit has one at most
+// (with more they are slower: 32x32, 11008x4096 at batch 32, 344 tiles, 15.6 us, 64x32
+// 13.1).  us, and what the rest of the rule gives: 32x16 4096x4096 at 17 7.0 and 9.5,
+// 1024x4096 at 128 6.4 and 8.8, gated at 32 5.7 and 8.8; 32x32 4096x4096 at 64 8.8
+// and 10.8, 8192x8192 at 17 15.0 and 17.4, gated 4096x4096 at 32 9.8 and 11.6; 32x64
+// 5001x4999 at 40 12.5 and 15.9, 1024x8192 at 400 13.3 and 15.5; 64x64 5001x4999 at
+// 128 18.6 and 21.2.  Not where splits of the columns, or two workgroups a unit with
+// one group of waves each, are better: 512x13824 at 77, 96 tiles of 32x32, 12.3 and
+// 10.6; 8192x22016 at 32 41.8 and 40.3; 32x64, 2000x13824 at 256 25.3 and 22.1; 64x64,
+// 3000x1024 at 200 6.6 and 5.8.
 Choice choose(int64_t rows, int64_t cols, int64_t batch, bool glu)
 {
     const int64_t blocks = sqllm_int8_cols(cols) / kBlock, m = glu ? 2 : 1;
     Choice best = {k256x256, 1, 0};
     double least = 1e30;
-    const int64_t of32 = (rows * m + 31) / 32 * ((batch + 31) / 32), of16 = (rows * m + 31) / 32 * ((batch + 15) / 16);
-    auto small = [&](int64_t tiles) { return tiles <= 256 && (blocks <= 64 || (blocks <= 128 && tiles > 128)); };
-    if (small(of16)) return {of16 <= 128 ? k32x16x4 : k32x16, 1, 0};
-    if (small(of32)) return {k32x32, 1, 0};
+    auto tiles = [&](int64_t tm, int64_t tn) { return (rows * m + tm - 1) / tm * ((batch + tn - 1) / tn); };
+    auto fits = [&](int64_t n) { return n <= 256 && (blocks <= 64 || (blocks <= 128 && n > 128)); };
+    if (fits(tiles(32, 16))) return {tiles(32, 16) <= 128 ? k32x16x4 : k32x16, 1, 0};
+    if (fits(tiles(32, 32))) return {k32x32, 1, 0};
+    if (blocks <= 64) {
+        if (blocks >= 16 && tiles(32, 64) <= 256) return {k32x64, 1, 0};
+        if (tiles(64, 32) <= 256) return {k64x32, 1, 0};
+        if (blocks > 32 && tiles(64, 64) <= 256) return {k64x64x3, 1, 0};
+    }
     for (int t = 0; t < kTiles; ++t) {
-        const int64_t mine = kTile[t].tm / m, tiles = ((rows + mine - 1) / mine) * ((batch + kTile[t].tn - 1) / kTile[t].tn);
+        const int64_t of = tiles(kTile[t].tm, kTile[t].tn);
         for (int64_t s = 1; s <= 8 && (s == 1 || (t > k256x256 && blocks >= 8 * s)); s *= 2) {
             const int64_t share = (blocks + s - 1) / s, splits = (blocks + share - 1) / share; // none empty
-            const int64_t wgs = tiles * splits, pairs = wgs / 512, rest = wgs % 512;
+            const int64_t wgs = of * splits, pairs = wgs / 512, rest = wgs % 512;
             double last = rest > 256 ? kTile[t].two : rest ? kTile[t].one : 0;
             if (rest > 256 && kTile[t].pairs) // some units have one: the loads of the others go faster
                 last = kTile[t].one + (kTile[t].two - kTile[t].one) * (rest - 256) / 256;
@@ -1057,6 +1064,10 @@ void launch_choice(const Choice &c, const Operands &p, int *partial, hipStream_t
         launch_tiled<GLU, 64, 64, 32, 32, 4, 1>(p, c.splits, partial, stream);
     } else if (c.tile == k64x32) {
         launch_tiled<GLU, 64, 32, 32, 16, 5, 1>(p, c.splits, partial, stream);
+    } else if (c.tile == k64x64x3) {
+        launch_tiled<GLU, 64, 64, 32, 32, 3, 3>(p, 1, nullptr, stream);
+    } else if (c.tile == k32x64) {
+        launch_tiled<GLU, 32, 64, 32, 16, 4, 2>(p, 1, nullptr, stream);
     } else if (c.tile == k32x32) {
         launch_tiled<GLU, 32, 32, 32, 16, 5, 2>(p, 1, nullptr, stream);
     } else if (c.tile == k32x16) {

@@ -119,7 +119,7 @@ FEW = [(17, 32, 100), (17, 33, 128), (20, 4097, 129), (32, 4096, 4096), (48, 270
        (26, 8465, 6456), (19, 4483, 16399), (17, 2097, 16542), (656, 778, 9159), (428, 577, 4998), (370, 216, 16669),
        (553, 466, 9433), (376, 342, 5449), (291, 141, 16682), (462, 1029, 9409), (451, 857, 7459), (401, 473, 16406),
        (437, 1745, 17094), (480, 433, 7598), (614, 179, 16510), (177, 2637, 11906), (708, 1185, 129), (620, 3281, 129),
-       (643, 1236, 11607), (545, 1848, 5886), (516, 3196, 129)]
+       (643, 1236, 11607), (545, 1848, 5886), (516, 3196, 129), (40, 10990, 4200), (130, 5001, 4999), (70, 2900, 8190)]
 
 
 @pytest.mark.parametrize("batch,rows,cols", FEW)

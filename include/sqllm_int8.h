@@ -76,6 +76,22 @@ sqllm_status sqllm_int8_glu(const int8_t *gate, const float *gate_scale, const i
                             int64_t rows, int64_t cols, const void *x, const float *xscale, int64_t batch, uint16_t *h,
                             void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/*
+ * Test-only export (not part of the stable contract).  sqllm_test_int8_plan:
+ * how sqllm_int8_gemm (gated: sqllm_int8_glu) would compute a product of these
+ * sizes, x in fp16 or (stored) in integers, without a device.  plan: HOST array
+ * of 5 ints:
+ *   plan[0]  1 if the quantiser's launch comes first
+ *   plan[1]  the form: 0 streaming in the vector units, 1 streaming on the
+ *            matrix cores, 2 tiles
+ *   plan[2]  rows of x the kernel holds (1, 2, 4); blocks of 128 columns a wave
+ *            (2, 4, 8, 16); the tile's number, 0 (256x256) to 10 (64x64 in three
+ *            groups of waves)
+ *   plan[3]  chunks of 1024 columns a wave (1 to 3); 0; splits of the columns
+ *   plan[4]  0; 0; whole 256x256 tiles in front of the halves (0: no halves)
+ */
+sqllm_status sqllm_test_int8_plan(int64_t rows, int64_t cols, int64_t batch, int gated, int stored, int *plan);
+
 #ifdef __cplusplus
 }
 #endif

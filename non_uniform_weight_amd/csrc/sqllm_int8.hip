@@ -937,17 +937,33 @@ Dot dot_shape(int64_t ld, int64_t batch)
     return {(total + 2) / 3, 3};
 }
 
-// Whether a streaming form takes the product.
-bool streams(int64_t cols, int64_t batch)
+int dot_rows(int64_t batch) { return batch > 2 ? 4 : (int)batch; } // rows of x that it is built for
+
+// How a product is computed.
+struct Plan {
+    Dot dot;      // the streaming form in the vector units, if it takes the product
+    bool inside;  // which rounds x in fp16 itself
+    int few;      // else blocks a wave of the one on the matrix cores, 0: not this form
+    Choice tiles; // else
+};
+
+Plan plan_of(int64_t rows, int64_t cols, int64_t batch, bool glu, bool stored)
 {
-    const int64_t ld = sqllm_int8_cols(cols);
-    return dot_shape(ld, batch).waves || (batch <= 16 && ld <= 192 * kBlock);
+    const int64_t ld = sqllm_int8_cols(cols), blocks = ld / kBlock;
+    Plan p = {dot_shape(ld, batch), false, 0, {k256x256, 1, 0}};
+    if (p.dot.waves)
+        p.inside = !stored && (batch <= 2 || p.dot.chunks == 1);
+    else if (batch <= 16 && blocks <= 192)
+        p.few = blocks <= 32 ? 2 : blocks <= 64 ? 4 : blocks <= 128 ? 8 : 16;
+    else
+        p.tiles = choose(rows, cols, batch, glu);
+    return p;
 }
 
 size_t workspace_bytes(int64_t rows, int64_t cols, int64_t batch, bool glu)
 {
     if (!good_sizes(rows, cols, batch)) return 0;
-    const int splits = streams(cols, batch) ? 1 : choose(rows, cols, batch, glu).splits;
+    const int splits = plan_of(rows, cols, batch, glu, false).tiles.splits;
     return up256((size_t)batch * sqllm_int8_cols(cols)) + up256((size_t)batch * 4) +
            (splits > 1 ? (size_t)splits * batch * partial_pitch(rows) * (glu ? 8 : 4) : 0);
 }
@@ -1000,9 +1016,10 @@ void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStrea
 template <bool GLU, bool HALF>
 void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStream_t stream)
 {
-    if (p.batch == 1)
+    const int held = dot_rows(p.batch);
+    if (held == 1)
         launch_dots<GLU, HALF, 1>(p, x, cols, d, stream);
-    else if (p.batch == 2)
+    else if (held == 2)
         launch_dots<GLU, HALF, 2>(p, x, cols, d, stream);
     else
         launch_dots<GLU, HALF, 4>(p, x, cols, d, stream);
@@ -1096,9 +1113,9 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
     float *const xs = (float *)(xq + up256((size_t)batch * ld));
     int *const partial = (int *)((uint8_t *)xs + up256((size_t)batch * 4));
     Operands p = {{q[0], q[1]}, {scale[0], scale[1]}, (const int8_t *)x, xscale, y, (int)rows, (int)batch, (int)(ld / kBlock)};
-    const Dot d = dot_shape(ld, batch);
-    if (d.waves && !xscale && (batch <= 2 || (batch <= 4 && d.chunks == 1))) {
-        launch_dots<GLU, true>(p, (const uint16_t *)x, (int)cols, d, stream);
+    const Plan plan = plan_of(rows, cols, batch, GLU, xscale != nullptr);
+    if (plan.inside) {
+        launch_dots<GLU, true>(p, (const uint16_t *)x, (int)cols, plan.dot, stream);
         return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
     }
     if (!xscale) {
@@ -1106,20 +1123,18 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
             return SQLLM_ERR_HIP;
         p.xq = xq, p.xscale = xs;
     }
-    if (d.waves) {
-        launch_dots<GLU, false>(p, nullptr, (int)cols, d, stream);
-    } else if (streams(cols, batch)) {
-        if (p.blocks <= 32)
-            launch_few<GLU, 2, 2>(p, stream);
-        else if (p.blocks <= 64)
-            launch_few<GLU, 4, 2>(p, stream);
-        else if (p.blocks <= 128)
-            launch_few<GLU, 8, 4>(p, stream);
-        else
-            launch_few<GLU, 16, 4>(p, stream);
-    } else {
-        launch_choice<GLU>(choose(rows, cols, batch, GLU), p, partial, stream);
-    }
+    if (plan.dot.waves)
+        launch_dots<GLU, false>(p, nullptr, (int)cols, plan.dot, stream);
+    else if (plan.few == 2)
+        launch_few<GLU, 2, 2>(p, stream);
+    else if (plan.few == 4)
+        launch_few<GLU, 4, 2>(p, stream);
+    else if (plan.few == 8)
+        launch_few<GLU, 8, 4>(p, stream);
+    else if (plan.few == 16)
+        launch_few<GLU, 16, 4>(p, stream);
+    else
+        launch_choice<GLU>(plan.tiles, p, partial, stream);
     return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
 }
 
@@ -1149,4 +1164,17 @@ extern "C" sqllm_status sqllm_int8_glu(const int8_t *gate, const float *gate_sca
 {
     return product<true>({gate, up}, {gate_scale, up_scale}, rows, cols, x, xscale, batch, h, workspace,
                          workspace_bytes, stream);
+}
+
+extern "C" sqllm_status sqllm_test_int8_plan(int64_t rows, int64_t cols, int64_t batch, int gated, int stored, int *plan)
+{
+    if (!plan) return SQLLM_ERR_NULL;
+    if (!good_sizes(rows, cols, batch)) return SQLLM_ERR_SHAPE;
+    const Plan p = plan_of(rows, cols, batch, gated != 0, stored != 0);
+    plan[0] = !stored && !p.inside;
+    plan[1] = p.dot.waves ? 0 : p.few ? 1 : 2;
+    plan[2] = p.dot.waves ? dot_rows(batch) : p.few ? p.few : p.tiles.tile;
+    plan[3] = p.dot.waves ? p.dot.chunks : p.few ? 0 : p.tiles.splits;
+    plan[4] = p.dot.waves || p.few ? 0 : p.tiles.whole;
+    return SQLLM_OK;
 }

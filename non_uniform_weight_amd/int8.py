@@ -23,9 +23,11 @@ _lib.sqllm_int8_gemm.restype = _i32
 _lib.sqllm_int8_gemm.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
 _lib.sqllm_int8_glu.restype = _i32
 _lib.sqllm_int8_glu.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
+_lib.sqllm_test_int8_plan.restype = _i32
+_lib.sqllm_test_int8_plan.argtypes = [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i32)]
 
 EXPORTS = ("sqllm_int8_cols", "sqllm_int8_quantize", "sqllm_int8_workspace_bytes", "sqllm_int8_glu_workspace_bytes",
-           "sqllm_int8_gemm", "sqllm_int8_glu")
+           "sqllm_int8_gemm", "sqllm_int8_glu", "sqllm_test_int8_plan")
 _MAX_COLS = 131071
 _gemm, _glu, _quantize = _lib.sqllm_int8_gemm, _lib.sqllm_int8_glu, _lib.sqllm_int8_quantize
 
@@ -118,3 +120,22 @@ def int8_glu(index, handle, gate: torch.Tensor, gate_scale: torch.Tensor, up: to
     _check(_calls.with_scratch(ws, int8_glu_workspace_bytes(rows, cols, batch), index, handle, _glu, gp, gsp, up_, usp,
                                rows, cols, xp, xsp, batch, hp), "sqllm_int8_glu")
     return h
+
+
+TILES = ("256x256", "256x128", "128x128", "128x64", "64x64", "64x32", "32x16", "32x16 in four groups", "32x32", "32x64",
+         "64x64 in three groups")
+
+
+def int8_plan(rows: int, cols: int, batch: int, gated: bool = False, stored: bool = False) -> dict:
+    """Test-only: how int8_gemm (gated: int8_glu) would compute a product, without a device.  rounded_first: whether
+    the quantiser's launch comes before; form: "vector" (with the rows of x the kernel holds and the chunks a wave
+    has), "matrix" (with the blocks a wave has) or "tiles" (with the tile, the splits of the columns and the whole
+    tiles in front of halves, 0 without)."""
+    out = (_i32 * 5)()
+    _check(_lib.sqllm_test_int8_plan(rows, cols, batch, gated, stored, out), "sqllm_test_int8_plan")
+    plan = {"rounded_first": bool(out[0]), "form": ("vector", "matrix", "tiles")[out[1]]}
+    if out[1] == 0:
+        return {**plan, "held": out[2], "chunks": out[3]}
+    if out[1] == 1:
+        return {**plan, "blocks": out[2]}
+    return {**plan, "tile": TILES[out[2]], "splits": out[3], "whole": out[4]}

@@ -939,6 +939,17 @@ Dot dot_shape(int64_t ld, int64_t batch)
 
 int dot_rows(int64_t batch) { return batch > 2 ? 4 : (int)batch; } // rows of x that it is built for
 
+// Whether it rounds x in fp16 itself, which takes registers; those that would
+// spill are given rounded x, a launch more.  us inside and after the quantiser:
+// 8192x22016, one row 33.2 and 38.1, two 35.7 and 38.7; spilling: at four rows 79
+// and 41; gated at two, 12 registers, 512x16500 11.8 and 9.3, 1024x17000 17.1 and
+// 12.0, 8192x22016 73.7 and 70.6, 8192x49152 146 and 142, but 8192x16500 55.0 and
+// 57.1, 28000x17000 163 and 165.
+constexpr bool rounds_inside(bool glu, int held, int chunks)
+{
+    return chunks == 1 || held == 1 || (held == 2 && (chunks == 2 || !glu));
+}
+
 // How a product is computed.
 struct Plan {
     Dot dot;      // the streaming form in the vector units, if it takes the product
@@ -952,7 +963,7 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t batch, bool glu, bool stored)
     const int64_t ld = sqllm_int8_cols(cols), blocks = ld / kBlock;
     Plan p = {dot_shape(ld, batch), false, 0, {k256x256, 1, 0}};
     if (p.dot.waves)
-        p.inside = !stored && (batch <= 2 || p.dot.chunks == 1);
+        p.inside = !stored && rounds_inside(glu, dot_rows(batch), p.dot.chunks);
     else if (batch <= 16 && blocks <= 192)
         p.few = blocks <= 32 ? 2 : blocks <= 64 ? 4 : blocks <= 128 ? 8 : 16;
     else
@@ -1001,15 +1012,14 @@ void launch_dot(const Operands &p, const uint16_t *x, int cols, int waves, hipSt
 
 // Rows of a group.  us at one row with 2, 4 and 8: 8192x8192, one chunk a wave,
 // 12.1, 11.8, 12.4; at four rows 15.7, 14.9, 16.2; 8192x22016, three chunks, 28.2
-// and 29.3 with 2 and 4.  x in fp16 takes registers: four rows with two chunks or
-// more spill (8192x22016 79 us), those go through the quantiser first (41).
+// and 29.3 with 2 and 4.
 template <bool GLU, bool HALF, int B>
 void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStream_t stream)
 {
     if (d.chunks == 1) launch_dot<GLU, HALF, B, 1, 4>(p, x, cols, d.waves, stream);
-    if constexpr (!HALF || B < 4)
+    if constexpr (!HALF || rounds_inside(GLU, B, 2))
         if (d.chunks == 2) launch_dot<GLU, HALF, B, 2, B == 1 ? 4 : 2>(p, x, cols, d.waves, stream);
-    if constexpr (!HALF || B < 4)
+    if constexpr (!HALF || rounds_inside(GLU, B, 3))
         if (d.chunks == 3) launch_dot<GLU, HALF, B, 3, 2>(p, x, cols, d.waves, stream);
 }
 

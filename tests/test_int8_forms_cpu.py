@@ -25,8 +25,8 @@ def kernels(gated):
     for held in (1, 2, 4):  # x in integers
         for chunks in (1, 2, 3):
             yield gated, "vector", False, held, chunks
-    inside = [(1, 1), (1, 2), (1, 3), (2, 1), (2, 2), (2, 3), (4, 1)]  # x in fp16, rounded in the kernel
-    for held, chunks in inside:
+    inside = [(1, 1), (1, 2), (1, 3), (2, 1), (2, 2), (4, 1)]  # x in fp16, rounded in the kernel
+    for held, chunks in inside if gated else [*inside, (2, 3)]:
         yield gated, "vector", True, held, chunks
     for blocks in (2, 4, 8, 16):
         yield gated, "matrix", blocks
@@ -52,6 +52,17 @@ def test_the_sizes_of_one_form_reach_it(gated):
             assert p["form"] == "vector" and p["chunks"] == (2 if cols <= 16384 else 3)
         elif gated:
             assert p == {"rounded_first": False, "form": "tiles", "tile": "256x128", "splits": 1, "whole": 0}
+
+
+@pytest.mark.parametrize("batch,cols,gemm,glu", [(1, 49152, False, False), (2, 16384, False, False), (2, 16385, False, True),
+                                                 (2, 49152, False, True), (3, 8192, False, False), (3, 8193, True, True),
+                                                 (4, 8192, False, False), (4, 20000, True, True), (5, 300, True, True)])
+def test_where_x_is_rounded(batch, cols, gemm, glu):
+    """x in fp16 is rounded in a launch before the product where the kernel that would do it has no registers left."""
+    for rows in (1, 300, 20000):
+        for gated, first in ((False, gemm), (True, glu)):
+            assert int8.int8_plan(rows, cols, batch, gated)["rounded_first"] is first
+            assert int8.int8_plan(rows, cols, batch, gated, stored=True)["rounded_first"] is False
 
 
 def test_plan_argument_errors():

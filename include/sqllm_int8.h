@@ -43,9 +43,13 @@ sqllm_status sqllm_int8_quantize(const uint16_t *x, int64_t rows, int64_t cols, 
                                  hipStream_t stream);
 
 /* Scratch bytes of the product, and of sqllm_int8_glu with two matrices of
- * that size; 0 if the sizes are out of range. */
+ * that size; 0 if the sizes are out of range.  The first two are for x in
+ * fp16, with room for its rounded form; with x in the stored form the calls
+ * ask for no more than the other two, 256 bytes where no columns are split. */
 size_t sqllm_int8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
 size_t sqllm_int8_glu_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
+size_t sqllm_int8_stored_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
+size_t sqllm_int8_glu_stored_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
 
 /*
  * sqllm_int8_gemm -- y = x W^T with W [rows][cols] in the stored form.

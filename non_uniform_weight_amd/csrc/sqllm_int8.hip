@@ -971,12 +971,23 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t batch, bool glu, bool stored)
     return p;
 }
 
-size_t workspace_bytes(int64_t rows, int64_t cols, int64_t batch, bool glu)
+// Scratch of a product: x in integers, unless it comes so, and the sums of splits.
+struct Scratch {
+    size_t codes, scales, sums;
+    size_t bytes() const { return std::max<size_t>(codes + scales + sums, 256); } // (0 says that sizes are out of range)
+};
+
+Scratch scratch_of(const Plan &p, int64_t rows, int64_t cols, int64_t batch, bool glu, bool stored)
+{
+    const int splits = p.tiles.splits;
+    return {stored ? 0 : up256((size_t)batch * sqllm_int8_cols(cols)), stored ? 0 : up256((size_t)batch * 4),
+            splits > 1 ? (size_t)splits * batch * partial_pitch(rows) * (glu ? 8 : 4) : 0};
+}
+
+size_t workspace_bytes(int64_t rows, int64_t cols, int64_t batch, bool glu, bool stored)
 {
     if (!good_sizes(rows, cols, batch)) return 0;
-    const int splits = plan_of(rows, cols, batch, glu, false).tiles.splits;
-    return up256((size_t)batch * sqllm_int8_cols(cols)) + up256((size_t)batch * 4) +
-           (splits > 1 ? (size_t)splits * batch * partial_pitch(rows) * (glu ? 8 : 4) : 0);
+    return scratch_of(plan_of(rows, cols, batch, glu, stored), rows, cols, batch, glu, stored).bytes();
 }
 
 template <bool GLU>
@@ -1116,19 +1127,20 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
     for (int k = 0; k < 2; ++k)
         if (!aligned(q[k], 16) || !aligned(scale[k], 4)) return SQLLM_ERR_ALIGN;
     if (!aligned(x, xscale ? 16 : 2) || !aligned(xscale, 4) || !aligned(y, 2)) return SQLLM_ERR_ALIGN;
-    if (!workspace || !aligned(workspace, 256) || workspace_size < workspace_bytes(rows, cols, batch, GLU))
-        return SQLLM_ERR_WORKSPACE;
+    const bool stored = xscale != nullptr;
+    const Plan plan = plan_of(rows, cols, batch, GLU, stored);
+    const Scratch scratch = scratch_of(plan, rows, cols, batch, GLU, stored);
+    if (!workspace || !aligned(workspace, 256) || workspace_size < scratch.bytes()) return SQLLM_ERR_WORKSPACE;
     const int64_t ld = sqllm_int8_cols(cols);
     int8_t *const xq = (int8_t *)workspace;
-    float *const xs = (float *)(xq + up256((size_t)batch * ld));
-    int *const partial = (int *)((uint8_t *)xs + up256((size_t)batch * 4));
+    float *const xs = (float *)(xq + scratch.codes);
+    int *const partial = (int *)((uint8_t *)xs + scratch.scales);
     Operands p = {{q[0], q[1]}, {scale[0], scale[1]}, (const int8_t *)x, xscale, y, (int)rows, (int)batch, (int)(ld / kBlock)};
-    const Plan plan = plan_of(rows, cols, batch, GLU, xscale != nullptr);
     if (plan.inside) {
         launch_dots<GLU, true>(p, (const uint16_t *)x, (int)cols, plan.dot, stream);
         return hipGetLastError() == hipSuccess ? SQLLM_OK : SQLLM_ERR_HIP;
     }
-    if (!xscale) {
+    if (!stored) {
         if (sqllm::launch_int8_quantize((const uint16_t *)x, batch, cols, cols, xq, xs, stream) != hipSuccess)
             return SQLLM_ERR_HIP;
         p.xq = xq, p.xscale = xs;
@@ -1152,12 +1164,22 @@ sqllm_status product(const int8_t *const (&q)[2], const float *const (&scale)[2]
 
 extern "C" size_t sqllm_int8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
 {
-    return workspace_bytes(rows, cols, batch, false);
+    return workspace_bytes(rows, cols, batch, false, false);
 }
 
 extern "C" size_t sqllm_int8_glu_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
 {
-    return workspace_bytes(rows, cols, batch, true);
+    return workspace_bytes(rows, cols, batch, true, false);
+}
+
+extern "C" size_t sqllm_int8_stored_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
+{
+    return workspace_bytes(rows, cols, batch, false, true);
+}
+
+extern "C" size_t sqllm_int8_glu_stored_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
+{
+    return workspace_bytes(rows, cols, batch, true, true);
 }
 
 extern "C" sqllm_status sqllm_int8_gemm(const int8_t *q, const float *scale, int64_t rows, int64_t cols, const void *x,

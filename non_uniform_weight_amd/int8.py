@@ -16,7 +16,8 @@ _lib.sqllm_int8_cols.restype = _i64
 _lib.sqllm_int8_cols.argtypes = [_i64]
 _lib.sqllm_int8_quantize.restype = _i32
 _lib.sqllm_int8_quantize.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
-for _size in (_lib.sqllm_int8_workspace_bytes, _lib.sqllm_int8_glu_workspace_bytes):
+for _size in (_lib.sqllm_int8_workspace_bytes, _lib.sqllm_int8_glu_workspace_bytes,
+              _lib.sqllm_int8_stored_workspace_bytes, _lib.sqllm_int8_glu_stored_workspace_bytes):
     _size.restype = _sz
     _size.argtypes = [_i64, _i64, _i64]
 _lib.sqllm_int8_gemm.restype = _i32
@@ -27,7 +28,8 @@ _lib.sqllm_test_int8_plan.restype = _i32
 _lib.sqllm_test_int8_plan.argtypes = [_i64, _i64, _i64, _i32, _i32, ctypes.POINTER(_i32)]
 
 EXPORTS = ("sqllm_int8_cols", "sqllm_int8_quantize", "sqllm_int8_workspace_bytes", "sqllm_int8_glu_workspace_bytes",
-           "sqllm_int8_gemm", "sqllm_int8_glu", "sqllm_test_int8_plan")
+           "sqllm_int8_stored_workspace_bytes", "sqllm_int8_glu_stored_workspace_bytes", "sqllm_int8_gemm",
+           "sqllm_int8_glu", "sqllm_test_int8_plan")
 _MAX_COLS = 131071
 _gemm, _glu, _quantize = _lib.sqllm_int8_gemm, _lib.sqllm_int8_glu, _lib.sqllm_int8_quantize
 
@@ -39,13 +41,17 @@ def int8_cols(cols: int) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def int8_workspace_bytes(rows: int, cols: int, batch: int) -> int:
-    return int(_lib.sqllm_int8_workspace_bytes(rows, cols, batch)) if _calls.held(_i64, rows, cols, batch) else 0
+def int8_workspace_bytes(rows: int, cols: int, batch: int, stored: bool = False) -> int:
+    """Scratch bytes of int8_gemm for x in fp16, or (stored) in integers with x_scale: far less."""
+    size = _lib.sqllm_int8_stored_workspace_bytes if stored else _lib.sqllm_int8_workspace_bytes
+    return int(size(rows, cols, batch)) if _calls.held(_i64, rows, cols, batch) else 0
 
 
 @functools.lru_cache(maxsize=4096)
-def int8_glu_workspace_bytes(rows: int, cols: int, batch: int) -> int:
-    return int(_lib.sqllm_int8_glu_workspace_bytes(rows, cols, batch)) if _calls.held(_i64, rows, cols, batch) else 0
+def int8_glu_workspace_bytes(rows: int, cols: int, batch: int, stored: bool = False) -> int:
+    """The same of int8_glu."""
+    size = _lib.sqllm_int8_glu_stored_workspace_bytes if stored else _lib.sqllm_int8_glu_workspace_bytes
+    return int(size(rows, cols, batch)) if _calls.held(_i64, rows, cols, batch) else 0
 
 
 @_calls.on_stream
@@ -93,13 +99,13 @@ def int8_gemm(index, handle, q: torch.Tensor, scale: torch.Tensor, x: torch.Tens
               y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """y fp16 [batch, rows] = x W^T for W stored as int8_quantize leaves it.  x: fp16 [batch, cols] (or [cols]),
     rounded inside; or, with x_scale (fp32 [batch]), int8 [batch, int8_cols(cols)].
-    ws: scratch of int8_workspace_bytes(rows, cols, batch) bytes (a cached one if None)."""
+    ws: scratch of int8_workspace_bytes(rows, cols, batch, stored=x_scale is not None) bytes (a cached one if None)."""
     qp, sp = _weights(q, scale, "q", index)
     rows, kept = q.shape
     batch, cols, xp, xsp = _activations(x, x_scale, kept, index)
     y, yp = _calls.output(y, "y", (batch, rows), torch.float16, index)
-    _check(_calls.with_scratch(ws, int8_workspace_bytes(rows, cols, batch), index, handle, _gemm, qp, sp, rows, cols, xp,
-                               xsp, batch, yp), "sqllm_int8_gemm")
+    _check(_calls.with_scratch(ws, int8_workspace_bytes(rows, cols, batch, xsp is not None), index, handle, _gemm, qp, sp,
+                               rows, cols, xp, xsp, batch, yp), "sqllm_int8_gemm")
     return y
 
 
@@ -109,7 +115,8 @@ def int8_glu(index, handle, gate: torch.Tensor, gate_scale: torch.Tensor, up: to
              ws: torch.Tensor | None = None) -> torch.Tensor:
     """h fp16 [batch, rows] = silu(x G^T) * (x U^T): both projections of a gated feed-forward block, the activation
     and the product in one call.  gate, up: as int8_quantize leaves them; x, x_scale: as int8_gemm's.
-    ws: scratch of int8_glu_workspace_bytes(rows, cols, batch) bytes (a cached one if None)."""
+    ws: scratch of int8_glu_workspace_bytes(rows, cols, batch, stored=x_scale is not None) bytes (a cached one if
+    None)."""
     gp, gsp = _weights(gate, gate_scale, "gate", index)
     up_, usp = _weights(up, up_scale, "up", index)
     if gate.shape != up.shape:
@@ -117,8 +124,8 @@ def int8_glu(index, handle, gate: torch.Tensor, gate_scale: torch.Tensor, up: to
     rows, kept = gate.shape
     batch, cols, xp, xsp = _activations(x, x_scale, kept, index)
     h, hp = _calls.output(h, "h", (batch, rows), torch.float16, index)
-    _check(_calls.with_scratch(ws, int8_glu_workspace_bytes(rows, cols, batch), index, handle, _glu, gp, gsp, up_, usp,
-                               rows, cols, xp, xsp, batch, hp), "sqllm_int8_glu")
+    _check(_calls.with_scratch(ws, int8_glu_workspace_bytes(rows, cols, batch, xsp is not None), index, handle, _glu, gp,
+                               gsp, up_, usp, rows, cols, xp, xsp, batch, hp), "sqllm_int8_glu")
     return h
 
 

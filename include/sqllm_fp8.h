@@ -47,8 +47,11 @@ int64_t sqllm_fp8_scale_pitch(int64_t cols);
 sqllm_status sqllm_fp8_quantize(const uint16_t *x, int64_t rows, int64_t cols, int64_t ldx, uint8_t *q,
                                 uint8_t *scale, hipStream_t stream);
 
-/* Scratch bytes of the product; 0 if the sizes are out of range. */
+/* Scratch bytes of the product of x in fp16, with room for its rounded form,
+ * and of x in the stored form: 256 where no columns are split.  0 if the sizes
+ * are out of range. */
 size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
+size_t sqllm_fp8_stored_workspace_bytes(int64_t rows, int64_t cols, int64_t batch);
 
 /*
  * sqllm_fp8_gemm -- y = x W^T with W [rows][cols] in the stored form and x
@@ -72,7 +75,8 @@ sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, int64_t rows
  * sqllm_fp8_gemm_stored -- the same with x already in the stored form, as
  * sqllm_fp8_quantize and sqllm_rms_norm_fp8 leave it: xq uint8 [batch]
  * [sqllm_fp8_cols(cols)], 16-byte aligned, xscale uint8 [batch]
- * [sqllm_fp8_scale_pitch(cols)], 4-byte aligned.
+ * [sqllm_fp8_scale_pitch(cols)], 4-byte aligned; scratch of
+ * sqllm_fp8_stored_workspace_bytes.
  */
 sqllm_status sqllm_fp8_gemm_stored(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
                                    const uint8_t *xq, const uint8_t *xscale, int64_t batch, uint16_t *y,

@@ -852,20 +852,27 @@ extern "C" size_t sqllm_fp8_workspace_bytes(int64_t rows, int64_t cols, int64_t 
            (splits > 1 ? (size_t)splits * batch * rows * 4 : 0);
 }
 
+// As launch_product splits.
+extern "C" size_t sqllm_fp8_stored_workspace_bytes(int64_t rows, int64_t cols, int64_t batch)
+{
+    if (!good_shape(rows, cols) || !good_shape(batch, cols) || !good_product(rows, batch)) return 0;
+    const int splits = streams(cols, batch) ? stream_splits(rows, sqllm_fp8_cols(cols) / kBlock) : choose(rows, cols, batch).splits;
+    return std::max<size_t>(splits > 1 ? (size_t)splits * batch * rows * 4 : 0, 256);
+}
+
 namespace {
 
-// What both products check alike; x: in either form, aligned to x_align.
+// What both products check alike; x: in either form, aligned to x_align; need: scratch bytes of sizes in range.
 sqllm_status check_product(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols, const void *x,
                            uintptr_t x_align, int64_t batch, const uint16_t *y, const void *workspace,
-                           size_t workspace_bytes)
+                           size_t workspace_bytes, size_t (*need)(int64_t, int64_t, int64_t))
 {
     if (!q || !scale || !x || !y) return SQLLM_ERR_NULL;
     if (!good_shape(rows, cols)) return SQLLM_ERR_SHAPE;
     if (!good_shape(batch, cols)) return SQLLM_ERR_BATCH;
     if (!good_product(rows, batch)) return SQLLM_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(scale, 4) || !aligned(x, x_align) || !aligned(y, 2)) return SQLLM_ERR_ALIGN;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < sqllm_fp8_workspace_bytes(rows, cols, batch))
-        return SQLLM_ERR_WORKSPACE;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need(rows, cols, batch)) return SQLLM_ERR_WORKSPACE;
     return SQLLM_OK;
 }
 
@@ -890,7 +897,8 @@ extern "C" sqllm_status sqllm_fp8_gemm(const uint8_t *q, const uint8_t *scale, i
                                        const uint16_t *x, int64_t batch, uint16_t *y, void *workspace,
                                        size_t workspace_bytes, hipStream_t stream)
 {
-    sqllm_status st = check_product(q, scale, rows, cols, x, 2, batch, y, workspace, workspace_bytes);
+    sqllm_status st = check_product(q, scale, rows, cols, x, 2, batch, y, workspace, workspace_bytes,
+                                    sqllm_fp8_workspace_bytes);
     if (st != SQLLM_OK) return st;
     uint8_t *xq = (uint8_t *)workspace, *xs = xq + up256((size_t)batch * sqllm_fp8_cols(cols));
     const Operands p = {q, scale, xq, xs, y, (int)rows, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
@@ -909,11 +917,11 @@ extern "C" sqllm_status sqllm_fp8_gemm_stored(const uint8_t *q, const uint8_t *s
                                               void *workspace, size_t workspace_bytes, hipStream_t stream)
 {
     if (!xscale) return SQLLM_ERR_NULL;
-    const sqllm_status st = check_product(q, scale, rows, cols, xq, 16, batch, y, workspace, workspace_bytes);
+    const sqllm_status st = check_product(q, scale, rows, cols, xq, 16, batch, y, workspace, workspace_bytes,
+                                          sqllm_fp8_stored_workspace_bytes);
     if (st != SQLLM_OK) return st;
     if (!aligned(xscale, 4)) return SQLLM_ERR_ALIGN;
     const Operands p = {q, scale, xq, xscale, y, (int)rows, (int)batch, (int)(sqllm_fp8_cols(cols) / kBlock),
                         (int)sqllm_fp8_scale_pitch(cols)};
-    // (the query's bytes hold the two parts of x first, here unused)
     return launch_product(p, cols, (float *)workspace, stream);
 }

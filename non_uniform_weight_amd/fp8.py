@@ -19,15 +19,16 @@ _lib.sqllm_fp8_scale_pitch.restype = _i64
 _lib.sqllm_fp8_scale_pitch.argtypes = [_i64]
 _lib.sqllm_fp8_quantize.restype = _i32
 _lib.sqllm_fp8_quantize.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
-_lib.sqllm_fp8_workspace_bytes.restype = _sz
-_lib.sqllm_fp8_workspace_bytes.argtypes = [_i64, _i64, _i64]
+for _size in (_lib.sqllm_fp8_workspace_bytes, _lib.sqllm_fp8_stored_workspace_bytes):
+    _size.restype = _sz
+    _size.argtypes = [_i64, _i64, _i64]
 _lib.sqllm_fp8_gemm.restype = _i32
 _lib.sqllm_fp8_gemm.argtypes = [_vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
 _lib.sqllm_fp8_gemm_stored.restype = _i32
 _lib.sqllm_fp8_gemm_stored.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _sz, _vp]
 
 EXPORTS = ("sqllm_fp8_cols", "sqllm_fp8_scale_pitch", "sqllm_fp8_quantize", "sqllm_fp8_workspace_bytes",
-           "sqllm_fp8_gemm", "sqllm_fp8_gemm_stored")
+           "sqllm_fp8_stored_workspace_bytes", "sqllm_fp8_gemm", "sqllm_fp8_gemm_stored")
 _gemm, _gemm_stored = _lib.sqllm_fp8_gemm, _lib.sqllm_fp8_gemm_stored
 
 
@@ -44,8 +45,10 @@ def fp8_scale_pitch(cols: int) -> int:
 
 
 @functools.lru_cache(maxsize=4096)
-def fp8_workspace_bytes(rows: int, cols: int, batch: int) -> int:
-    return int(_lib.sqllm_fp8_workspace_bytes(rows, cols, batch)) if _calls.held(_i64, rows, cols, batch) else 0
+def fp8_workspace_bytes(rows: int, cols: int, batch: int, stored: bool = False) -> int:
+    """Scratch bytes of fp8_gemm for x in fp16, or (stored) in e4m3 with x_scale: far less."""
+    size = _lib.sqllm_fp8_stored_workspace_bytes if stored else _lib.sqllm_fp8_workspace_bytes
+    return int(size(rows, cols, batch)) if _calls.held(_i64, rows, cols, batch) else 0
 
 
 @_calls.on_stream
@@ -71,7 +74,7 @@ def fp8_gemm(index, handle, q: torch.Tensor, scale: torch.Tensor, x: torch.Tenso
              ws: torch.Tensor | None = None, *, x_scale: torch.Tensor | None = None) -> torch.Tensor:
     """y [batch, rows] = x W^T for fp16 x [batch, cols] (or [cols]) and W stored as fp8_quantize leaves it; with
     x_scale, x and x_scale are in that form too (as rms_norm_fp8 leaves them).
-    ws: scratch of fp8_workspace_bytes(rows, cols, batch) bytes (a cached one if None)."""
+    ws: scratch of fp8_workspace_bytes(rows, cols, batch, stored=x_scale is not None) bytes (a cached one if None)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x: torch.Tensor expected")
     if x.dim() == 1:
@@ -95,6 +98,6 @@ def fp8_gemm(index, handle, q: torch.Tensor, scale: torch.Tensor, x: torch.Tenso
     else:
         call, name, xs = _gemm, "sqllm_fp8_gemm", (_calls.address(x, "x", torch.float16, index),)
     y, yp = _calls.output(y, "y", (batch, rows), torch.float16, index)
-    _check(_calls.with_scratch(ws, fp8_workspace_bytes(rows, cols, batch), index, handle, call, qp, sp, rows, cols, *xs,
-                               batch, yp), name)
+    _check(_calls.with_scratch(ws, fp8_workspace_bytes(rows, cols, batch, x_scale is not None), index, handle, call, qp, sp,
+                               rows, cols, *xs, batch, yp), name)
     return y

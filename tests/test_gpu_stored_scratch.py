@@ -65,3 +65,35 @@ def test_integer_products_hold_no_room_for_x():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want[0]) and torch.equal(h, want[1])
+
+
+# batch, rows, cols: streaming, tiles, and both with split columns
+@pytest.mark.parametrize("batch,rows,cols", [(1, 5000, 9000), (3, 300, 9001), (16, 1000, 16400), (12, 8200, 8300), (16, 500, 2048),
+                                             (40, 300, 6000), (100, 300, 16500), (300, 600, 5001), (600, 5000, 400)])
+def test_e4m3_product(batch, rows, cols):
+    """The bits that the call gives with a full workspace, in bytes of the smaller one between guards."""
+    step(f"fp8 stored scratch batch {batch} {rows}x{cols}")
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    q, scale = nw().fp8_quantize((torch.randn(rows, cols, generator=g, device="cuda") * 0.02).half())
+    xq, xs = nw().fp8_quantize(base.acts(batch, cols, 1))
+    full = torch.empty(nw().fp8_workspace_bytes(rows, cols, batch), dtype=torch.uint8, device="cuda")
+    want = nw().fp8_gemm(q, scale, xq, x_scale=xs, ws=full)
+    need = nw().fp8_workspace_bytes(rows, cols, batch, stored=True)
+    buf, ws = scratch(need)
+    assert torch.equal(nw().fp8_gemm(q, scale, xq, x_scale=xs, ws=ws), want)
+    assert kept(buf, need)
+    assert torch.equal(nw().fp8_gemm(q, scale, xq, x_scale=xs), want)
+
+
+def test_e4m3_product_holds_no_room_for_x():
+    step("fp8 stored scratch kept")
+    rows, cols, batch = 256, 8192, 4096
+    q, scale = nw().fp8_quantize(base.acts(rows, cols, 1))
+    xq, xs = nw().fp8_quantize(base.acts(batch, cols, 3))
+    y = torch.empty(batch, rows, dtype=torch.float16, device="cuda")
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    nw().fp8_gemm(q, scale, xq, x_scale=xs, y=y, stream=stream)
+    stream.synchronize()
+    assert torch.cuda.memory_allocated() - before <= 1 << 20

@@ -40,3 +40,22 @@ def test_integer_products(rows, cols, batch, call, query, words):
 def test_sizes_out_of_range(query):
     assert query(0, 300, 1, stored=True) == query(64, 131072, 1, stored=True) == query(64, 300, 0, stored=True) == 0
     assert query(1 << 20, 300, 1 << 19, stored=True) == query(64 + 2 ** 64, 300, 3, stored=True) == 0
+
+
+def fp8(rows, cols, batch, size, ws=A):
+    return LIB.sqllm_fp8_gemm_stored(A, B, rows, cols, A, B, batch, B, ws, size, None)
+
+
+@pytest.mark.parametrize("rows,cols,batch", SIZES)
+def test_e4m3_product(rows, cols, batch):
+    need = nw.fp8_workspace_bytes(rows, cols, batch, stored=True)
+    assert need == 256 or any(need == splits * batch * rows * 4 for splits in range(2, 9))
+    assert nw.fp8_workspace_bytes(rows, cols, batch) >= batch * nw.fp8_cols(cols) + (need if need > 256 else 0)
+    assert fp8(rows, cols, batch, need - 1) == fp8(rows, cols, batch, need, None) == 8
+    assert fp8(rows, cols, batch, need, P(0x100080)) == 8
+
+
+def test_e4m3_sizes_out_of_range():
+    query = nw.fp8_workspace_bytes
+    assert query(0, 300, 1, stored=True) == query(64, 1 << 25, 1, stored=True) == query(64, 300, 0, stored=True) == 0
+    assert query(1 << 20, 300, 1 << 19, stored=True) == query(64 + 2 ** 64, 300, 3, stored=True) == 0

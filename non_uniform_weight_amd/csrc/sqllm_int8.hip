@@ -161,15 +161,19 @@ __device__ __forceinline__ bool tile_of(const Operands &p, int wg, int first, in
 // (row % 8), so that the sixteen rows that a fragment read takes at one piece
 // lie in different banks; loads into LDS write lane after lane, so the swizzle
 // is in the address they read from.
-// What bounds small tiles: a compute unit takes in 145 bytes/ns out of its L2, but
-// 28 to 31 of W from memory.  64x32 tiles, 8192x8192 at batch 64, with four stages
-// 20.6 us, five and six 19.5, twelve 20.4; with every workgroup beginning at
-// another block, so that they read other channels, 19.6 to 25.  32 rows of W a tile
-// halve what a unit takes of it (at batch 17 15.4 us, in 64x32 tiles 18.2, with
-// split columns 17.6).  Their steps are short chains of latencies, so a workgroup has
-// G groups of waves: a stage is G blocks, one for each group, whose sums are added
-// through LDS at the end.  32x16 tiles, 1024x8192 at batch 32, with four groups 7.8
-// us, with two 9.1; at 256 tiles (4096x4096) 7.2 and 7.0.
+// What bounds small tiles is neither memory nor the matrix cores.  By the counters
+// W comes from memory once and x once for each XCD (8192x8192 at batch 256 84.0 MB,
+// 83.9 needed): workgroups with the same rows of W do share them in their L2.  That
+// is 4.1 TB/s at batch 17 and 2.4 at 256, with the matrix cores busy 7 and 23% of
+// the time.  Waves stand at a wait for a third to a half of their cycles and before
+// the issue of an instruction for a quarter to a third more: a stage is a short
+// chain of latencies.  What was tried on it: 64x32 tiles, 8192x8192 at batch 64,
+// with four stages 20.6 us, five and six 19.5, twelve 20.4; with every workgroup
+// beginning at another block 19.6 to 25; 32 rows of W a tile, at batch 17, 15.4 us,
+// in 64x32 tiles 18.2, with split columns 17.6.  So that more chains run side by
+// side, a workgroup has G groups of waves: a stage is G blocks, one for each group,
+// whose sums are added through LDS at the end.  32x16 tiles, 1024x8192 at batch 32,
+// with four groups 7.8 us, with two 9.1; at 256 tiles (4096x4096) 7.2 and 7.0.
 template <int TM, int TN, int WM, int WN, int S, int G>
 struct Tiling {
     static constexpr int W = (TM / WM) * (TN / WN); // waves of a group
@@ -298,11 +302,12 @@ __global__ void __launch_bounds__(64 * (TM / WM) * (TN / WN) * G, 2) gemm_tiled(
 // after the next in that step and the one behind it, then W of the block after
 // that.  SPLIT: a workgroup has a share of the blocks, and the sums go to
 // partial[split][product][batch][rows].
-// 8192x8192 at batch 4096 takes 219 us (2500 TOP/s; 427 with 64x64 tiles).  The
-// matrix instructions alone take 171 on random operands, 124 on zeros: the clock
-// falls with their power; with the reads from LDS 176, with the loads 198.  The
-// rest is a tile's ends: 3 us to its first block, 5 from its last to the last
-// store, 3 of those for 256 conversions a lane.
+// 8192x8192 at batch 4096 takes 205 to 221 us on different cards (2500 TOP/s and
+// more; 427 with 64x64 tiles).  Where it took 219, the matrix instructions alone
+// took 171 on random operands, 124 on zeros: the clock falls with their power; with
+// the reads from LDS 176, with the loads 198.  The rest is a tile's ends: 3 us to
+// its first block, 5 from its last to the last store, 3 of those for 256
+// conversions a lane.
 template <int FM, int FN>
 struct Large {
     static constexpr int kW = 64 * FM * kBlock, kX = 64 * FN * kBlock;
@@ -538,9 +543,10 @@ __device__ __forceinline__ int sum_of_16(int v)
 // one is used, and the waves' sums meet in LDS.  HALF: x comes in fp16.  Each
 // lane rounds the columns that it holds, once, while the first rows of W are on
 // their way; the largest of a row of x comes from all waves through LDS.
-// Memory bounds it: 8192x22016 at one row 28.4 us (6.4 TB/s; x in fp16 32.7),
-// 8192x8192 11.8, gate and up of 11008x4096 16.0 and of 22016x8192 55 (6.5 TB/s);
-// tiles took 46, 21 and 27.
+// Memory bounds it: 8192x22016 at one row 28.4 us (6.4 TB/s), 8192x8192 11.8, gate
+// and up of 11008x4096 16.0 and of 22016x8192 55 (6.5 TB/s); tiles took 46, 21 and
+// 27.  From matrices that were not read just before, on another card, 35.1 (x in
+// fp16 33.2), 14.5 and 19.1.
 constexpr int kChunk = 1024;
 
 template <bool GLU, bool HALF, int B, int C, int R>
@@ -705,8 +711,8 @@ __global__ void __launch_bounds__(1024) gemm_dot(Operands p, const uint16_t *x, 
 // ring of D blocks of its own, loaded straight from memory, whole lines of eight
 // rows an instruction (in the matrix cores' layout it would be 64 bytes of
 // sixteen), D blocks ahead and on into the next group.
-// 8192x8192 at 16 rows takes 16.5 us, at one in the form above 11.8: every
-// workgroup reads x first, 33 MB in all out of the second-level caches, and that
+// 8192x8192 at 16 rows takes 16.5 us from memory (12.4 of a matrix that is in the
+// 256 MB cache), at one in the form above 11.8: every workgroup reads x first, 33 MB in all out of the second-level caches, and that
 // is 3 us before W comes at its rate.  W through registers into LDS in half
 // kilobytes of a row took 17.5, x through the ring in turn with the first blocks
 // 16.3 and more registers, W asked for before x 16.8 to 17.8.
@@ -847,7 +853,10 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // 8192x8192, 64 blocks a tile, at 256 and 512 tiles: 256x256 at batch 2048 118 us
 // and at 4096 219; 256x128 at 1024 67, at 2048 132; 128x128 at 512 45, at 1024
 // 73; 128x64 at 256 36, at 512 67; 64x64 at 128 25.5, at 256 40; 64x32 at 64
-// 19.5, at 128 31.0.
+// 19.5, at 128 31.0.  A tile's ends (its first loads, the sums' way out; 10 us of
+// a round of 256x256) are in these times as parts of its blocks: where columns are
+// few, large tiles take longer than the rule thinks (8192x256 at batch 4096, two
+// rounds of two blocks, 27 us for 6.7; 8192x768 40 for 20).
 enum Tile { k256x256, k256x128, k128x128, k128x64, k64x64, k64x32, kTiles, k32x16 = kTiles, k32x16x4, k32x32, k32x64, k64x64x3 };
 constexpr struct {
     int tm, tn;
@@ -950,7 +959,11 @@ constexpr bool rounds_inside(bool glu, int held, int chunks)
     return chunks == 1 || held == 1 || (held == 2 && (chunks == 2 || !glu));
 }
 
-// How a product is computed.
+// How a product is computed.  The form on the matrix cores takes up to sixteen
+// rows of x whatever W is, one workgroup to 16 rows of W: 8192x8192 at 16 and, in
+// tiles, at 17 rows 16.8 and 18.2 us, 1024x8192 7.6 and 7.6, but where rows are
+// few and long, split tiles are faster: 256x24576 at 5, 16 and 17 11.0, 16.8 and
+// 11.4, 512x16384 8.4, 12.2 and 10.0, 1024x24576 15.7, 21.9 and 13.5.
 struct Plan {
     Dot dot;      // the streaming form in the vector units, if it takes the product
     bool inside;  // which rounds x in fp16 itself
@@ -964,7 +977,7 @@ Plan plan_of(int64_t rows, int64_t cols, int64_t batch, bool glu, bool stored)
     Plan p = {dot_shape(ld, batch), false, 0, {k256x256, 1, 0}};
     if (p.dot.waves)
         p.inside = !stored && rounds_inside(glu, dot_rows(batch), p.dot.chunks);
-    else if (batch <= 16 && blocks <= 192)
+    else if (batch <= 16 && blocks <= 192) // (however few units it fills)
         p.few = blocks <= 32 ? 2 : blocks <= 64 ? 4 : blocks <= 128 ? 8 : 16;
     else
         p.tiles = choose(rows, cols, batch, glu);
@@ -1048,7 +1061,8 @@ void launch_dots(const Operands &p, const uint16_t *x, int cols, Dot d, hipStrea
 
 // Blocks a wave and ring, us at 16 rows.  8192x8192: 4 blocks, ring of 2 16.3, of
 // 4 16.5, 8 blocks, 8 17.3, 4 18.8, 16 blocks 23.8; 4096x4096: 2 blocks 6.6, 4
-// 7.0, 8 7.3; gated 11008x4096: 18.1, 20.2, 22.1.
+// 7.0, 8 7.3; gated 11008x4096: 18.1, 20.2, 22.1.  Gated with 16 blocks a wave it
+// spills ten registers, which do not show: 8192x24576 94 to 96, ungated 50.
 template <bool GLU, int S, int D>
 void launch_few(const Operands &p, hipStream_t stream)
 {
